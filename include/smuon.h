@@ -56,6 +56,9 @@ typedef int32_t smuon_status;
                          bits past the last entry zero; ld must equal cols and data be 16-byte aligned.
                          A set bit is the sign +1 (u >= 0), a clear bit -1 */
 
+#define SMUON_E4M3 4  /* 8-bit floating codes (4 exponent bits, 3 mantissa bits, largest 448, no infinity):
+                         the 8-bit moments of adamw_state, and nothing else */
+
 /* bits OR-ed into *d_status by device code */
 #define SMUON_DEV_NONFINITE_NORM 1  /* a Frobenius norm (or a spectral-norm estimate) was NaN or Inf */
 #define SMUON_DEV_WAIT_TIMEOUT   2  /* a bounded pipeline wait ran out; results invalid */
@@ -452,6 +455,107 @@ smuon_status lionmuon_step(lionmuon_state* st, int32_t P, float beta1, float bet
                            float a, float b, float c, int32_t iters, int8_t tie_value,
                            uint32_t ns_flags, const smuon_mat* G, void* ws, size_t ws_bytes,
                            int32_t* d_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW for the parameters that are not orthogonalised (embeddings, output
+ * head, norm gains, biases), or for a whole model.
+ *
+ * Not one of the pages' methods; the step is that of Loshchilov and Hutter,
+ * "Decoupled Weight Decay Regularization" (ICLR 2019), algorithm 2. For step
+ * t (1-indexed), with s the gradient factor (1 without one):
+ *   g  = s G
+ *   m' = b1 m + (1 - b1) g,   v' = b2 v + (1 - b2) g^2,   r' = sqrt(v')
+ *   W' = W - lr (wd W + (m' / (1 - b1^t)) / (r' / sqrt(1 - b2^t) + eps))
+ * in float32; W' is rounded to nearest even into W's type. g, m', v' and r'
+ * have every operation rounded on its own, in the order
+ *   f32(s G),  f32(f32(b1 m) + f32(f32(1 - b1) g)),
+ *   f32(f32(b2 v) + f32(f32(1 - b2) f32(g g))),  f32(sqrt(v')),
+ * so the moments have the same bits in any IEEE evaluation. No result depends
+ * on the grid, the GPU or how the tensors are split into launches.
+ *
+ * Tensors. W and G may have a row stride (ld > cols); master, m and v are the
+ * optimizer's own and must be contiguous (ld == cols). rows and cols may be
+ * any non-negative int32 (a tensor with no entries is skipped, and its data
+ * may be NULL). No limit on n_tensors; up to 320 tensors of one combination of
+ * types go into one launch.
+ *
+ * 8-bit moments (m and v of type SMUON_E4M3). m holds the first moment, v the
+ * square root of the second (a code spans 2^16 of a block's values, enough
+ * for gradients' sizes, not for their squares). Blocks of 256 consecutive
+ * entries of a tensor's row-major flattening (the last one may be short) share
+ * one exponent byte per moment, scales[i][2 * block + {0 m, 1 root}]: the
+ * float32 exponent field of the block's largest magnitude less 7; 0 for a block
+ * of zeros (largest magnitude below 2^-119), 255 for a block that holds a NaN
+ * or an infinity. A value is code * 2^(byte - 127) (0, respectively NaN, in
+ * the last two cases); so zero bytes everywhere are zero moments. m' and r'
+ * are rounded stochastically: with y = x * 2^(127 - byte), 16 random bits are
+ * added at bit 4 of y's float32 pattern, the pattern is cut to three mantissa
+ * bits and the result converted to E4M3 (to nearest, below 2^-6 the codes are
+ * 2^-9 apart). Rounding to nearest would lose nearly every change of v: with
+ * b2 = 0.999 its root moves by 0.05% in a step, a code step is 6 to 12%. The
+ * random bits of entry e of tensor i (one number for both moments) are half
+ * e % 2 of word (e % 8) / 2 of Philox4x32-10 at counter (e / 8 low word, e / 8
+ * high word, t, 1), key (seed, i): a run is a function of its inputs and its
+ * seed. W' uses m' and r' before they are rounded to 8 bits.
+ *
+ * Non-finite gradients make their entries' W and moments (8 bits: the moments
+ * of their block) non-finite; d_skip_if with smuon_grad_norm drops such steps.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t          n_tensors;
+  uint32_t         seed;         /* of the 8-bit moments' rounding */
+  const smuon_mat* W;            /* [n] F32 or BF16, updated in place */
+  const smuon_mat* master;       /* nullable [n]: F32 originals of BF16 weights; entries with data == NULL: none.
+                                    The step is taken on the master, W receives it rounded */
+  const smuon_mat* m;            /* [n] first moments, all F32 or all SMUON_E4M3 */
+  const smuon_mat* v;            /* [n] second moments, F32; or SMUON_E4M3: their square roots */
+  uint8_t* const*  scales;       /* SMUON_E4M3: [n] device pointers, ceil(entries / 256) * 2 bytes, 2-byte aligned */
+  const float*     lr_scale;     /* nullable host [n]: factors on lr */
+  const float*     weight_decay; /* nullable host [n]: wd (NULL: 0) */
+  int64_t          t;            /* steps taken; a call runs step t + 1 and increments it (also when *d_skip_if != 0) */
+  int64_t*         d_t;          /* nullable device int64[2], {steps taken, 0}: the count that is used instead of t. A step
+                                    increments it unless it is skipped, so replays of a captured step count on */
+} adamw_state;
+
+/* One step. lr, beta1, beta2 and eps are doubles because 1 - beta2 and the bias corrections need their digits.
+ *  G[n]          gradients, F32 or BF16, shapes of W. Several entries may share memory; none may overlap a written
+ *                tensor, and no two written tensors may overlap (SMUON_ERR_INVALID_ARG).
+ *  lr            learning rate >= 0 (ignored with d_lr: device float, read when the step runs)
+ *  beta1, beta2  in [0, 1);  eps > 0
+ *  d_grad_scale  nullable device float: s (d_out + 1 of smuon_grad_norm)
+ *  d_skip_if     nullable device int32: when nonzero at run time the step leaves everything as it was
+ * Steps on one state run one after another (on one stream, or ordered by events). */
+smuon_status adamw_step(adamw_state* st, const smuon_mat* G, double lr, double beta1, double beta2, double eps,
+                        const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if, void* stream);
+
+/* The step prepared once: the addresses in st and G, beta1, beta2, eps and the device pointers are kept (also
+ * weight_decay and lr_scale as they are now); adamw_execute takes t and the learning rate anew (st->t is incremented;
+ * st->d_t and st->seed are those of creation). Executing is capturable; a captured step counts on only with d_t. */
+smuon_status adamw_plan_create(const adamw_state* st, const smuon_mat* G, double beta1, double beta2, double eps,
+                               const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if,
+                               smuon_plan* out);
+smuon_status adamw_execute(smuon_plan plan, adamw_state* st, double lr, void* stream);
+
+/* dst's moments <- src's moments, from F32 to SMUON_E4M3 or back (the other direction of types, or two states of one
+ * type, are SMUON_ERR_DTYPE; tensor i of both must have the same number of entries). To 8 bits values are rounded to
+ * nearest even code. dst->t <- src->t; with device counts (both states have one, or neither) the count is copied on
+ * the stream. Weights are not touched. */
+smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* stream);
+
+/* Global 2-norm of n gradients, on the device: d_out[0] = norm, d_out[1] = min(1, max_norm / (norm + 1e-6)), the factor
+ * that clips the gradients to max_norm (> 0; infinity: never clips). Where the norm is not a finite float32, d_out[1] =
+ * 0, *d_skip = 1 (else 0; nullable) and SMUON_DEV_NONFINITE_NORM is OR-ed into *d_status (nullable). Squares are summed
+ * in float32 over eight entries and in float64 above, in a fixed order; every gradient whose norm float32 holds gets it,
+ * however small or large its entries. G as in adamw_step (F32 and BF16 may be mixed; n_tensors >= 1). ws: scratch of
+ * smuon_grad_norm_workspace_bytes(), 256-byte aligned, not shared with a call that may run concurrently. The plan form
+ * keeps ws, the addresses and max_norm. */
+smuon_status smuon_grad_norm_workspace_bytes(const smuon_mat* G, int32_t n_tensors, size_t* bytes);
+smuon_status smuon_grad_norm(const smuon_mat* G, int32_t n_tensors, double max_norm, float* d_out, int32_t* d_skip,
+                             void* ws, size_t ws_bytes, int32_t* d_status, void* stream);
+smuon_status smuon_grad_norm_plan_create(const smuon_mat* G, int32_t n_tensors, double max_norm, float* d_out,
+                                         int32_t* d_skip, void* ws, size_t ws_bytes, int32_t* d_status,
+                                         smuon_plan* out);
+smuon_status smuon_grad_norm_execute(smuon_plan plan, void* stream);
 
 #ifdef __cplusplus
 }

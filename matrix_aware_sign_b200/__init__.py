@@ -12,14 +12,14 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsmuon.so")
 
-F32, BF16, I8, BITS = 0, 1, 2, 3
+F32, BF16, I8, BITS, E4M3 = 0, 1, 2, 3, 4
 NS_FP32_REF, NS_SPLIT_BF16, NS_NO_NORMALIZE, NS_EMIT_Q, NS_SIMT_BF16 = 1, 2, 4, 8, 16
 NS_GRAM_ONLY = 32  # CacheMuon fresh solve iterated on the m x m Gram (with NS_EMIT_Q, one matrix)
 NS_SPECTRAL = 64  # spectral-norm normalisation X_0 = M / (||M||_2 + eps) (Lanczos estimate on the device)
@@ -71,6 +71,14 @@ class LionMuonState(ctypes.Structure):
                 ("mom", POINTER(SmuonMat)), ("t", c_int64), ("grad", POINTER(GradStream))]
 
 
+class AdamWState(ctypes.Structure):
+    """adamw_state (the binding's AdamW fills it)."""
+    _fields_ = [("n_tensors", c_int32), ("seed", c_uint32), ("W", POINTER(SmuonMat)), ("master", POINTER(SmuonMat)),
+                ("m", POINTER(SmuonMat)), ("v", POINTER(SmuonMat)), ("scales", POINTER(c_void_p)),
+                ("lr_scale", POINTER(c_float)), ("weight_decay", POINTER(c_float)), ("t", c_int64),
+                ("d_t", c_void_p)]
+
+
 _lib = None
 
 
@@ -116,6 +124,18 @@ def lib() -> ctypes.CDLL:
             "lionmuon_step": (c_int32, [POINTER(LionMuonState), c_int32, c_float, c_float, c_float, c_float,
                                         c_float, c_float, c_int32, c_int8, c_uint32, M, c_void_p, c_size_t,
                                         c_void_p, c_void_p]),
+            "adamw_step": (c_int32, [POINTER(AdamWState), M, c_double, c_double, c_double, c_double, c_void_p,
+                                     c_void_p, c_void_p, c_void_p]),
+            "adamw_plan_create": (c_int32, [POINTER(AdamWState), M, c_double, c_double, c_double, c_void_p, c_void_p,
+                                            c_void_p, POINTER(c_void_p)]),
+            "adamw_execute": (c_int32, [c_void_p, POINTER(AdamWState), c_double, c_void_p]),
+            "adamw_convert": (c_int32, [POINTER(AdamWState), POINTER(AdamWState), c_void_p]),
+            "smuon_grad_norm_workspace_bytes": (c_int32, [M, c_int32, POINTER(c_size_t)]),
+            "smuon_grad_norm": (c_int32, [M, c_int32, c_double, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
+                                          c_void_p]),
+            "smuon_grad_norm_plan_create": (c_int32, [M, c_int32, c_double, c_void_p, c_void_p, c_void_p, c_size_t,
+                                                      c_void_p, POINTER(c_void_p)]),
+            "smuon_grad_norm_execute": (c_int32, [c_void_p, c_void_p]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -424,3 +444,240 @@ def smuon_harness_gaussian(G, workers: int, stream_desc: GradStream, step: int, 
         raise ValueError("len(G) must be a multiple of workers")
     _check(lib().smuon_harness_gaussian(_mats(G), n // workers, workers, ctypes.byref(stream_desc), step,
                                         _stream(stream)))
+
+
+# ---------------------------------------------------------------- AdamW and gradient norm
+_DT_TENSOR = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+
+
+def tensor(t) -> SmuonMat:
+    """Describes a tensor of any shape for the AdamW calls: contiguous, or 2-D with unit column stride."""
+    if t.dtype not in _DT_TENSOR:
+        raise ValueError(f"dtype {t.dtype} is not supported")
+    n, ptr, dt = t.numel(), t.data_ptr(), _DT_TENSOR[t.dtype]
+    if n == 0:
+        return SmuonMat(None, 0, 0, 0, dt)
+    if t.is_contiguous():
+        cols = t.shape[-1] if t.dim() else 1
+        if max(cols, n // cols) >= 1 << 31:
+            raise ValueError("at most 2^31 - 1 rows and columns: view the tensor in another shape")
+        return SmuonMat(ptr, n // cols, cols, cols, dt)
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError("tensors must be contiguous, or 2-D with unit column stride and rows that do not overlap")
+    return SmuonMat(ptr, t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1], dt)
+
+
+def _tensors(ts, shapes=None, name="G"):
+    ts = list(ts)
+    if shapes is not None:
+        if len(ts) != len(shapes):
+            raise ValueError(f"{len(ts)} tensors in {name}, {len(shapes)} weights")
+        for i, (t, s) in enumerate(zip(ts, shapes)):
+            if t is not None and tuple(t.shape) != s:
+                raise ValueError(f"{name}[{i}] has shape {tuple(t.shape)}, its weight {s}")
+    return (SmuonMat * len(ts))(*[SmuonMat() if t is None else tensor(t) for t in ts])
+
+
+def _one_device(*groups) -> torch.device:
+    """The CUDA device that all tensors are on; ValueError otherwise."""
+    devs = {t.device for g in groups if g is not None for t in g if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError(f"tensors must be on one CUDA device, got {sorted(map(str, devs))}")
+    return next(iter(devs))
+
+
+def _scalar(t, dtype, name):
+    if t is not None and (t.dtype != dtype or t.numel() != 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of one element")
+    return t
+
+
+class AdamW:
+    """Weights, moments and step count of an AdamW run over many tensors: the
+    parameters beside the matrices that the Muon-type steps take, or a whole
+    model.
+
+    W             weights, float32 or bfloat16, any shapes (contiguous, or 2-D
+                  with a row stride), updated in place by adamw_step
+    bits          32: float32 moments. 8: E4M3 codes with one power-of-two
+                  exponent per 256 entries, stochastically rounded from `seed`
+                  and the step (include/smuon.h states the format)
+    m, v, scales  existing moments instead of zeros (float32, or float8_e4m3fn
+                  with uint8 `scales` of shape (ceil(entries / 256), 2); v then
+                  holds the second moment's square root)
+    master        True: a float32 original is kept for every bfloat16 weight
+                  and stepped in its place; or a list of them (None: none)
+    weight_decay, lr_scale   one number, or one per tensor
+    t             steps taken
+    device_step   keep the count on the device: a step that is skipped does not
+                  count, and replays of a captured step count on
+    """
+
+    def __init__(self, W, m=None, v=None, scales=None, master=None, bits=32, weight_decay=0.0, lr_scale=1.0, seed=0,
+                 t=0, device_step=False):
+        self.W = list(W)
+        n = len(self.W)
+        shapes = [tuple(w.shape) for w in self.W]
+        if (m is None) != (v is None) or (m is None and scales is not None):
+            raise ValueError("give m and v together (with scales for 8-bit moments), or none of them")
+        if m is None:
+            if bits not in (8, 32):
+                raise ValueError("bits must be 8 or 32")
+            kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+            zeros = lambda: [torch.zeros(w.numel() * (4 if bits == 32 else 1), dtype=torch.uint8, device=w.device)  # noqa: E731
+                             .view(kind).view(w.shape) for w in self.W]
+            m, v = zeros(), zeros()
+            if bits == 8:
+                scales = [torch.zeros((-(-w.numel() // 256), 2), dtype=torch.uint8, device=w.device) for w in self.W]
+        self.m, self.v = list(m), list(v)
+        self.bits = 8 if self.m and self.m[0].dtype == torch.float8_e4m3fn else 32
+        if (self.bits == 8) != (scales is not None):
+            raise ValueError("scales go with 8-bit moments, and only with them")
+        self.scales = None if scales is None else list(scales)
+        if self.scales is not None:
+            if len(self.scales) != n:
+                raise ValueError(f"{len(self.scales)} scales, {n} weights")
+            for i, (s, w) in enumerate(zip(self.scales, self.W)):
+                if s.dtype != torch.uint8 or not s.is_contiguous() or s.numel() != 2 * -(-w.numel() // 256):
+                    raise ValueError(f"scales[{i}] must be a contiguous uint8 tensor of shape (ceil(entries / 256), 2)")
+        if master is True:
+            master = [w.detach().float().contiguous() if w.dtype == torch.bfloat16 else None for w in self.W]
+        self.master = None if not master else list(master)
+        self.device = _one_device(self.W, self.m, self.v, self.scales, self.master)
+        self._shapes = shapes
+        per = lambda x: (c_float * n)(*(x if isinstance(x, (list, tuple)) else [x] * n))  # noqa: E731
+        for x, name in ((weight_decay, "weight_decay"), (lr_scale, "lr_scale")):
+            if isinstance(x, (list, tuple)) and len(x) != n:
+                raise ValueError(f"{len(x)} values of {name}, {n} weights")
+        self._arrays = (_tensors(self.W), None if self.master is None else _tensors(self.master, shapes, "master"),
+                        _tensors(self.m, shapes, "m"), _tensors(self.v, shapes, "v"),
+                        None if self.scales is None else (c_void_p * n)(*[s.data_ptr() for s in self.scales]),
+                        per(lr_scale), per(weight_decay))
+        self.d_t = torch.tensor([t, 0], dtype=torch.int64, device=self.device) if device_step else None
+        W_, master_, m_, v_, scales_, ls_, wd_ = self._arrays
+        self.state = AdamWState(n, seed, W_, master_, m_, v_, scales_, ls_, wd_, t, _ptr(self.d_t))
+
+    @property
+    def t(self) -> int:
+        """Steps taken (with device_step: waits for the device)."""
+        return self.state.t if self.d_t is None else int(self.d_t[0])
+
+
+def _adamw_args(opt, G, lr, grad_scale, skip_if):
+    G = list(G)
+    d_lr = _scalar(lr, torch.float32, "lr") if isinstance(lr, torch.Tensor) else None
+    _scalar(grad_scale, torch.float32, "grad_scale")
+    _scalar(skip_if, torch.int32, "skip_if")
+    mats = _tensors(G, opt._shapes)
+    if _one_device(G, [d_lr, grad_scale, skip_if]) != opt.device:
+        raise ValueError("the gradients are on another device than the weights")
+    return mats, d_lr
+
+
+def adamw_step(opt: AdamW, G, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=None, skip_if=None, stream=None):
+    """One AdamW step on all tensors of `opt`. G: gradients of the weights'
+    shapes, float32 or bfloat16. lr: a number, or a one-element float32 device
+    tensor read when the step runs. grad_scale: one-element float32 device
+    tensor that multiplies the gradients (GradNorm.coef). skip_if: one-element
+    int32 device tensor; nonzero leaves everything as it was (GradNorm.skip)."""
+    mats, d_lr = _adamw_args(opt, G, lr, grad_scale, skip_if)
+    with torch.cuda.device(opt.device):
+        _check(lib().adamw_step(ctypes.byref(opt.state), mats, 0.0 if d_lr is not None else lr, beta1, beta2, eps,
+                                _ptr(d_lr), _ptr(grad_scale), _ptr(skip_if), _stream(stream)))
+
+
+class AdamWPlan:
+    """adamw_step prepared once, for gradients that keep their addresses; run()
+    enqueues only the kernels. `lr` may be a device tensor here, or a number in run()."""
+
+    def __init__(self, opt: AdamW, G, beta1=0.9, beta2=0.999, eps=1e-8, lr=None, grad_scale=None, skip_if=None):
+        if lr is not None and not isinstance(lr, torch.Tensor):
+            raise ValueError("lr must be a device tensor here: give a number to run()")
+        mats, d_lr = _adamw_args(opt, G, lr, grad_scale, skip_if)
+        self.opt, self.tensors = opt, (list(G), d_lr, grad_scale, skip_if)  # keep the buffers alive
+        h = c_void_p()
+        with torch.cuda.device(opt.device):
+            _check(lib().adamw_plan_create(ctypes.byref(opt.state), mats, beta1, beta2, eps, _ptr(d_lr),
+                                           _ptr(grad_scale), _ptr(skip_if), ctypes.byref(h)))
+        self.handle, self._state, self._index = h, ctypes.byref(opt.state), opt.device.index
+
+    def run(self, lr=None, stream=None):
+        if (lr is None) != (self.tensors[1] is not None):
+            raise ValueError("give lr once: as a device tensor to the plan, or as a number here")
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.run(lr, stream)
+        _check(lib().adamw_execute(self.handle, self._state, 0.0 if lr is None else lr, _stream(stream)))
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h and _lib is not None:
+            _lib.smuon_plan_destroy(h)
+            self.handle = None
+
+
+def adamw_convert(src: AdamW, dst: AdamW, stream=None):
+    """dst's moments and step count <- src's, from 32 bits to 8 (rounded to nearest) or back."""
+    if src.device != dst.device:
+        raise ValueError("the two states are on different devices")
+    with torch.cuda.device(src.device):
+        _check(lib().adamw_convert(ctypes.byref(src.state), ctypes.byref(dst.state), _stream(stream)))
+
+
+def smuon_grad_norm_workspace_bytes(G) -> int:
+    G = list(G)
+    out = c_size_t(0)
+    _check(lib().smuon_grad_norm_workspace_bytes(_tensors(G), len(G), ctypes.byref(out)))
+    return out.value
+
+
+class GradNorm:
+    """Global 2-norm of many gradients, prepared once; run() enqueues only the
+    kernels. On the device afterwards: norm, coef = min(1, max_norm / (norm +
+    1e-6)) (one-element float32 tensors) and skip (int32: 1 where the norm is
+    not finite; coef is then 0)."""
+
+    def __init__(self, G, max_norm: float, status=None):
+        G = list(G)
+        self.device = _one_device(G, [status])
+        self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
+        self.norm, self.coef = self.out[0], self.out[1]
+        self.skip = torch.zeros((), dtype=torch.int32, device=self.device)
+        self.ws = workspace(smuon_grad_norm_workspace_bytes(G), self.device)
+        self.tensors = (G, _scalar(status, torch.int32, "status"))  # keep the buffers alive
+        h = c_void_p()
+        with torch.cuda.device(self.device):
+            _check(lib().smuon_grad_norm_plan_create(_tensors(G), len(G), max_norm, self.out.data_ptr(),
+                                                     self.skip.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+                                                     _ptr(status), ctypes.byref(h)))
+        self.handle = h
+
+    def run(self, stream=None):
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.run(stream)
+        _check(lib().smuon_grad_norm_execute(self.handle, _stream(stream)))
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h and _lib is not None:
+            _lib.smuon_plan_destroy(h)
+            self.handle = None
+
+
+def smuon_grad_norm(G, max_norm: float, out, skip=None, ws=None, status=None, stream=None):
+    """The norm of G into out (float32, two elements: norm, clip factor) and the
+    skip flag (int32), without a plan. Returns the workspace used: keep it until
+    the work on `stream` is done."""
+    G = list(G)
+    if out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous float32 tensor of two elements")
+    _scalar(skip, torch.int32, "skip")
+    _scalar(status, torch.int32, "status")
+    dev = _one_device(G, [out, skip, ws, status])
+    if ws is None:
+        ws = workspace(smuon_grad_norm_workspace_bytes(G), dev)
+    with torch.cuda.device(dev):
+        _check(lib().smuon_grad_norm(_tensors(G), len(G), max_norm, out.data_ptr(), _ptr(skip), ws.data_ptr(),
+                                     ws.numel(), _ptr(status), _stream(stream)))
+    return ws

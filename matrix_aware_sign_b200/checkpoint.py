@@ -2,8 +2,10 @@
 
 The whole state of a run is device tensors and step counters: the weights,
 every simulated worker's momentum (or LionMuon EMA), the step count t that
-selects Muon steps and the counter-based gradient streams, and for CacheMuon
-the cached transform Q, the current momentum and the counters. Nothing else
+selects Muon steps and the counter-based gradient streams, for CacheMuon
+the cached transform Q, the current momentum and the counters, and for AdamW
+the moments (8-bit ones as their codes and exponents), the float32 originals
+and the seed of the rounding. Nothing else
 carries over between steps, so restoring those bytes into the same buffers
 and continuing gives exactly the run that never stopped.
 
@@ -15,7 +17,7 @@ from __future__ import annotations
 
 import torch
 
-from . import CacheMuon, LionMuon
+from . import AdamW, CacheMuon, LionMuon
 
 
 def _sync(named) -> None:
@@ -43,6 +45,12 @@ def _tensors(obj):
     if isinstance(obj, CacheMuon):
         named = {"M": obj.M, "D": obj.D, "Q": obj.Q, "err": obj.err, "accept": obj.accept, "counters": obj.cnt}
         return "cachemuon", named, {"steps": int(obj.steps)}
+    if isinstance(obj, AdamW):
+        named = {f"{k}.{i}": x for k in ("W", "master", "m", "v", "scales")
+                 for i, x in enumerate(getattr(obj, k) or []) if x is not None}
+        if obj.d_t is not None:
+            named["t"] = obj.d_t
+        return "adamw", named, {"t": int(obj.state.t), "seed": int(obj.state.seed)}
     if isinstance(obj, dict):
         return "tensors", dict(obj), {}
     raise TypeError(f"cannot checkpoint a {type(obj).__name__}")
@@ -62,9 +70,11 @@ def restore(obj, snap: dict) -> None:
         raise ValueError(f"checkpoint of a {snap['kind']} run cannot resume a {kind} run")
     if set(snap["tensors"]) != set(named):
         raise ValueError("checkpoint and run hold different tensors")
+    if kind == "adamw" and snap["counters"]["seed"] != obj.state.seed:
+        raise ValueError("checkpoint and run round their moments from different seeds")
     for k, v in named.items():
         _put(v, snap["tensors"][k], k)
-    if kind == "lionmuon":
+    if kind in ("lionmuon", "adamw"):
         obj.state.t = snap["counters"]["t"]
     elif kind == "cachemuon":
         obj.steps = snap["counters"]["steps"]

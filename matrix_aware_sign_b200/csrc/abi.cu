@@ -6,6 +6,7 @@
 // stage kernels on the caller's stream. The host never reads device data.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -17,6 +18,7 @@
 #include <string>
 #include <vector>
 
+#include "adamw.cuh"
 #include "epilogue.cuh"
 
 using namespace smuon;
@@ -173,7 +175,9 @@ smuon_status encode_f32_3d(CUtensorMap* out, const void* ptr, int64_t inner, int
 }
 
 // ------------------------------------------------------------------ validation
-int dtype_size(int32_t dt) { return dt == SMUON_F32 ? 4 : dt == SMUON_BF16 ? 2 : dt == SMUON_I8 ? 1 : 0; }
+int dtype_size(int32_t dt) {
+  return dt == SMUON_F32 ? 4 : dt == SMUON_BF16 ? 2 : dt == SMUON_I8 || dt == SMUON_E4M3 ? 1 : 0;
+}
 
 smuon_status check_mat(const smuon_mat& m, const char* what, int i, bool allow_f32, bool allow_bf16,
                        bool allow_i8, bool allow_bits = false) {
@@ -1278,11 +1282,356 @@ smuon_status run_update(const UpdExec& ex, cudaStream_t s) {
 
 }  // namespace
 
+// ------------------------------------------------------------------ AdamW, gradient norm
+namespace {
+
+// A C entry point lets no C++ exception out: the only one that can arise is a failed host allocation.
+template <class F>
+smuon_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(SMUON_ERR_UNSUPPORTED, "host memory ran out (%s)", e.what());
+  }
+}
+
+// A tensor of the AdamW calls: any non-negative shape; data may be NULL without entries.
+smuon_status check_tensor(const smuon_mat& a, const char* what, int i, int32_t d0, int32_t d1, bool strided) {
+  if (a.rows < 0 || a.cols < 0) return fail(SMUON_ERR_SHAPE, "%s[%d] has shape %dx%d", what, i, a.rows, a.cols);
+  if (a.dtype != d0 && a.dtype != d1) return fail(SMUON_ERR_DTYPE, "%s[%d] has an unsupported dtype %d", what, i, a.dtype);
+  if (a.ld < a.cols) return fail(SMUON_ERR_SHAPE, "%s[%d].ld=%lld < cols=%d", what, i, (long long)a.ld, a.cols);
+  if (a.ld > ((int64_t)1 << 40)) return fail(SMUON_ERR_SHAPE, "%s[%d].ld=%lld is too large", what, i, (long long)a.ld);
+  if (!strided && a.rows > 1 && a.ld != a.cols)
+    return fail(SMUON_ERR_SHAPE, "%s[%d] must be contiguous (ld=%lld, cols=%d)", what, i, (long long)a.ld, a.cols);
+  const int64_t n = (int64_t)a.rows * a.cols;
+  if (n > ((int64_t)1 << 38)) return fail(SMUON_ERR_SHAPE, "%s[%d] has more than 2^38 entries", what, i);
+  if (n && !a.data) return fail(SMUON_ERR_INVALID_ARG, "%s[%d].data is NULL", what, i);
+  if (reinterpret_cast<uintptr_t>(a.data) % dtype_size(a.dtype) != 0)
+    return fail(SMUON_ERR_INVALID_ARG, "%s[%d].data is not aligned to its element size", what, i);
+  return SMUON_OK;
+}
+
+int64_t entries(const smuon_mat& a) { return (int64_t)a.rows * a.cols; }
+int64_t blocks_of(int64_t n) { return (n + kAdBlock - 1) / kAdBlock; }
+bool has_stride(const smuon_mat& a) { return a.rows > 1 && a.ld != a.cols; }
+
+// whether every eight entries from a multiple of eight on are one aligned vector: 32 bytes of F32, 16 of BF16, 8 codes
+bool vec8(const smuon_mat& a) {
+  const int bytes = 8 * dtype_size(a.dtype);
+  return reinterpret_cast<uintptr_t>(a.data) % bytes == 0 && (!has_stride(a) || (a.cols % 8 == 0 && a.ld % 8 == 0));
+}
+
+// memory that a call reads or writes: rows of row_bytes, pitch bytes apart
+struct Span {
+  uintptr_t lo, hi, row, pitch;
+  bool many, written;
+  const char* what;
+  int i;
+};
+
+void add_span(std::vector<Span>& v, const smuon_mat& a, bool written, const char* what, int i) {
+  if (entries(a) == 0) return;
+  const uintptr_t es = dtype_size(a.dtype), p = reinterpret_cast<uintptr_t>(a.data);
+  v.push_back(Span{p, p + ((uintptr_t)(a.rows - 1) * a.ld + a.cols) * es, a.cols * es, (uintptr_t)a.ld * es, a.rows > 1,
+                   written, what, i});
+}
+
+// b starts at or after a. Two column ranges of one matrix interleave without meeting.
+bool meet(const Span& a, const Span& b) {
+  if (b.lo >= a.hi) return false;
+  if (!a.many) return true;
+  if (b.many && b.pitch != a.pitch) return true;
+  const uintptr_t d = (b.lo - a.lo) % a.pitch;
+  return d < a.row || d + b.row > a.pitch;
+}
+
+smuon_status check_overlap(std::vector<Span>& v) {
+  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  // spans still open at v[j]: read ones are compared with written ones only
+  std::vector<size_t> open;
+  for (size_t j = 0; j < v.size(); ++j) {
+    size_t keep = 0;
+    for (size_t k : open) {
+      if (v[k].hi <= v[j].lo) continue;
+      open[keep++] = k;
+      if ((v[k].written || v[j].written) && meet(v[k], v[j]))
+        return fail(SMUON_ERR_INVALID_ARG, "%s[%d] and %s[%d] overlap", v[k].what, v[k].i, v[j].what, v[j].i);
+    }
+    open.resize(keep);
+    open.push_back(j);
+  }
+  return SMUON_OK;
+}
+
+struct AdExec {
+  struct Part {  // one launch
+    int kind;
+    bool few;
+    double bytes;
+    std::unique_ptr<AdTable<kAdFew>> small;
+    std::unique_ptr<AdTable<kAdMany>> large;
+  };
+  std::vector<Part> parts;
+  AdHyper h{};
+  DevInfo di;
+};
+
+const char* adamw_name(int kind) { return kind & AD_8BIT ? "k_adamw_8bit" : "k_adamw_32bit"; }
+
+// shapes and types of a state's moments, weights and masters; *eight: 8-bit moments
+smuon_status check_state(const adamw_state* st, bool* eight) {
+  if (!st || !st->W || !st->m || !st->v) return fail(SMUON_ERR_INVALID_ARG, "state, W, m and v must not be NULL");
+  if (st->n_tensors < 1) return fail(SMUON_ERR_INVALID_ARG, "n_tensors < 1");
+  if (st->t < 0) return fail(SMUON_ERR_INVALID_ARG, "t < 0");
+  const int32_t held = st->m[0].dtype;
+  *eight = held == SMUON_E4M3;
+  if (held != SMUON_F32 && held != SMUON_E4M3)
+    return fail(SMUON_ERR_DTYPE, "m[0] has an unsupported dtype %d (F32 or E4M3)", held);
+  if (*eight && !st->scales) return fail(SMUON_ERR_INVALID_ARG, "8-bit moments need scales");
+  if (reinterpret_cast<uintptr_t>(st->d_t) % 8) return fail(SMUON_ERR_INVALID_ARG, "d_t must be 8-byte aligned");
+  for (int i = 0; i < st->n_tensors; ++i) {
+    smuon_status s;
+    if ((s = check_tensor(st->W[i], "W", i, SMUON_F32, SMUON_BF16, true)) != SMUON_OK) return s;
+    if ((s = check_tensor(st->m[i], "m", i, held, held, false)) != SMUON_OK) return s;
+    if ((s = check_tensor(st->v[i], "v", i, held, held, false)) != SMUON_OK) return s;
+    const int64_t n = entries(st->W[i]);
+    if (entries(st->m[i]) != n || entries(st->v[i]) != n)
+      return fail(SMUON_ERR_SHAPE, "m[%d] or v[%d] differs from W[%d] in its number of entries", i, i, i);
+    if (st->master && st->master[i].data) {
+      if ((s = check_tensor(st->master[i], "master", i, SMUON_F32, SMUON_F32, false)) != SMUON_OK) return s;
+      if (st->W[i].dtype != SMUON_BF16) return fail(SMUON_ERR_DTYPE, "master[%d]: W[%d] is not BF16", i, i);
+      if (entries(st->master[i]) != n)
+        return fail(SMUON_ERR_SHAPE, "master[%d] differs from W[%d] in its number of entries", i, i);
+    }
+    if (*eight && n) {
+      if (!st->scales[i]) return fail(SMUON_ERR_INVALID_ARG, "scales[%d] is NULL", i);
+      if (reinterpret_cast<uintptr_t>(st->scales[i]) % 2)
+        return fail(SMUON_ERR_INVALID_ARG, "scales[%d] must be 2-byte aligned", i);
+    }
+  }
+  return SMUON_OK;
+}
+
+void add_moments(std::vector<Span>& v, const adamw_state* st, int i, bool eight, bool written) {
+  add_span(v, st->m[i], written, "m", i);
+  add_span(v, st->v[i], written, "v", i);
+  if (eight) {
+    const int64_t n = entries(st->W[i]);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(st->scales[i]);
+    if (n) v.push_back(Span{p, p + 2 * (uintptr_t)blocks_of(n), 0, 0, false, written, "scales", i});
+  }
+}
+
+smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double beta1, double beta2, double eps,
+                           const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if, AdExec* ex) {
+  bool eight = false;
+  smuon_status s = check_state(st, &eight);
+  if (s != SMUON_OK) return s;
+  if (!G) return fail(SMUON_ERR_INVALID_ARG, "G is NULL");
+  if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1))
+    return fail(SMUON_ERR_INVALID_ARG, "beta1=%g and beta2=%g must be in [0, 1)", beta1, beta2);
+  if (!((float)eps >= 1e-30f && eps < 1e30)) return fail(SMUON_ERR_INVALID_ARG, "eps=%g must be in 1e-30..1e30", eps);
+  const uintptr_t misaligned = (reinterpret_cast<uintptr_t>(d_lr) | reinterpret_cast<uintptr_t>(d_grad_scale) |
+                                reinterpret_cast<uintptr_t>(d_skip_if)) % 4;
+  if (misaligned) return fail(SMUON_ERR_INVALID_ARG, "d_lr, d_grad_scale and d_skip_if must be 4-byte aligned");
+  std::vector<Span> spans;
+  std::vector<std::vector<AdTensor>> by_kind(AD_KINDS);
+  for (int i = 0; i < st->n_tensors; ++i) {
+    const smuon_mat& W = st->W[i];
+    if ((s = check_tensor(G[i], "G", i, SMUON_F32, SMUON_BF16, true)) != SMUON_OK) return s;
+    if (!same_shape(G[i], W)) return fail(SMUON_ERR_SHAPE, "G[%d] differs from W[%d] in shape", i, i);
+    const float wd = st->weight_decay ? st->weight_decay[i] : 0.f, ls = st->lr_scale ? st->lr_scale[i] : 1.f;
+    if (!(wd >= 0.f && wd <= 1e30f && ls >= 0.f && ls <= 1e30f))
+      return fail(SMUON_ERR_INVALID_ARG, "weight_decay[%d]=%g and lr_scale[%d]=%g must be finite and >= 0", i, wd, i, ls);
+    const int64_t n = entries(W);
+    if (!n) continue;
+    const bool master = st->master && st->master[i].data;
+    add_span(spans, W, true, "W", i);
+    add_span(spans, G[i], false, "G", i);
+    if (master) add_span(spans, st->master[i], true, "master", i);
+    add_moments(spans, st, i, eight, true);
+    AdTensor T{};
+    T.w = W.data; T.g = G[i].data; T.m = st->m[i].data; T.v = st->v[i].data;
+    T.master = master ? reinterpret_cast<float*>(st->master[i].data) : nullptr;
+    T.scales = eight ? st->scales[i] : nullptr;
+    T.n = n; T.cols = W.cols; T.w_ld = W.ld; T.g_ld = G[i].ld;
+    T.lr_scale = ls; T.wd = wd; T.id = (uint32_t)i;
+    T.flags = (has_stride(W) ? kAdWStride : 0) | (has_stride(G[i]) ? kAdGStride : 0);
+    if (vec8(W) && vec8(G[i]) && vec8(st->m[i]) && vec8(st->v[i]) && (!master || vec8(st->master[i]))) T.flags |= kAdVec;
+    const int kind = (master ? AD_W_MASTER : W.dtype == SMUON_BF16 ? AD_W_BF16 : AD_W_F32) |
+                     (G[i].dtype == SMUON_BF16 ? AD_G_BF16 : 0) | (eight ? AD_8BIT : 0);
+    by_kind[kind].push_back(T);
+  }
+  if (st->d_t) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(st->d_t);
+    spans.push_back(Span{p, p + 16, 0, 0, false, true, "d_t", 0});
+  }
+  if ((s = check_overlap(spans)) != SMUON_OK) return s;
+  if ((s = device_info(&ex->di)) != SMUON_OK) return s;
+  ex->parts.clear();
+  for (int kind = 0; kind < AD_KINDS; ++kind) {
+    const std::vector<AdTensor>& ts = by_kind[kind];
+    const double w_bytes = (kind & 3) == AD_W_F32 ? 8 : (kind & 3) == AD_W_BF16 ? 4 : 10;
+    const double per = w_bytes + (kind & AD_G_BF16 ? 2 : 4) + (eight ? 4 : 16);
+    for (size_t i = 0; i < ts.size();) {
+      size_t j = i;
+      int64_t blocks = 0;
+      while (j < ts.size() && j - i < (size_t)kAdMany && blocks + blocks_of(ts[j].n) < ((int64_t)1 << 30) + 1)
+        blocks += blocks_of(ts[j++].n);
+      AdExec::Part P;
+      P.kind = kind;
+      P.few = j - i <= (size_t)kAdFew;
+      P.bytes = 0;
+      AdTensor* dst;
+      if (P.few) {
+        P.small.reset(new AdTable<kAdFew>());
+        P.small->n_tensors = (int32_t)(j - i);
+        P.small->total_blocks = (int32_t)blocks;
+        dst = P.small->t;
+      } else {
+        P.large.reset(new AdTable<kAdMany>());
+        P.large->n_tensors = (int32_t)(j - i);
+        P.large->total_blocks = (int32_t)blocks;
+        dst = P.large->t;
+      }
+      int32_t begin = 0;
+      for (; i < j; ++i, ++dst) {
+        *dst = ts[i];
+        dst->block_begin = begin;
+        begin += (int32_t)blocks_of(ts[i].n);
+        P.bytes += per * (double)ts[i].n + (eight ? 4.0 * (double)blocks_of(ts[i].n) : 0.0);
+      }
+      ex->parts.push_back(std::move(P));
+    }
+  }
+  if (ex->parts.empty() && st->d_t) {  // no entries at all: the count still advances
+    AdExec::Part P;
+    P.kind = AD_W_F32;
+    P.few = true;
+    P.bytes = 16;
+    P.small.reset(new AdTable<kAdFew>());
+    ex->parts.push_back(std::move(P));
+  }
+  AdHyper& h = ex->h;
+  h.skip = d_skip_if; h.d_lr = d_lr; h.d_gscale = d_grad_scale; h.d_t = st->d_t;
+  h.log_b1 = std::log(beta1); h.log_b2 = std::log(beta2);
+  h.b1 = (float)beta1; h.c1 = (float)(1.0 - beta1);
+  h.b2 = (float)beta2; h.c2 = (float)(1.0 - beta2);
+  h.eps = (float)eps;
+  h.seed = st->seed;
+  return SMUON_OK;
+}
+
+smuon_status run_adamw(const AdExec& ex, adamw_state* st, double lr, cudaStream_t s) {
+  if (st->t < 0) return fail(SMUON_ERR_INVALID_ARG, "t < 0");
+  if (!ex.h.d_lr && !(lr >= 0 && lr <= 1e30)) return fail(SMUON_ERR_INVALID_ARG, "lr=%g must be finite and >= 0", lr);
+  AdHyper h = ex.h;
+  h.t = st->t + 1;
+  h.lr = (float)lr;
+  for (size_t i = 0; i < ex.parts.size(); ++i) {
+    const AdExec::Part& P = ex.parts[i];
+    h.advance = i + 1 == ex.parts.size();
+    Launch L(adamw_name(P.kind), SMUON_WORK_BYTES, P.bytes, s);
+    CUDA_TRY(P.few ? launch_adamw<kAdFew>(P.kind, *P.small, h, ex.di.sms, s)
+                   : launch_adamw<kAdMany>(P.kind, *P.large, h, ex.di.sms, s));
+  }
+  st->t += 1;
+  return SMUON_OK;
+}
+
+struct NormExec {
+  std::vector<std::unique_ptr<NormTable>> tables;
+  std::vector<double> bytes;
+  NormOut o{};
+  DevInfo di;
+};
+
+smuon_status check_norm_tensors(const smuon_mat* G, int32_t n) {
+  if (!G) return fail(SMUON_ERR_INVALID_ARG, "G is NULL");
+  if (n < 1) return fail(SMUON_ERR_INVALID_ARG, "n_tensors < 1");
+  for (int i = 0; i < n; ++i) {
+    smuon_status s = check_tensor(G[i], "G", i, SMUON_F32, SMUON_BF16, true);
+    if (s != SMUON_OK) return s;
+  }
+  return SMUON_OK;
+}
+
+// launches of a norm over G, with their partial sums' place in ws (host only: ws NULL to size it)
+void norm_tables(const smuon_mat* G, int32_t n, double* ws, std::vector<std::unique_ptr<NormTable>>* out,
+                 std::vector<double>* bytes, int32_t* n_partials) {
+  *n_partials = 0;
+  std::unique_ptr<NormTable> tb;
+  int64_t blocks = 0;
+  double by = 0;
+  auto flush = [&] {
+    if (!tb) return;
+    tb->total_blocks = (int32_t)blocks;
+    tb->partials = ws ? ws + *n_partials : nullptr;
+    *n_partials += norm_grid(tb->total_blocks);
+    out->push_back(std::move(tb));
+    bytes->push_back(by);
+    blocks = 0;
+    by = 0;
+  };
+  for (int i = 0; i < n; ++i) {
+    const int64_t e = entries(G[i]);
+    if (!e) continue;
+    if (tb && (tb->n_tensors == kNormMany || blocks + blocks_of(e) > ((int64_t)1 << 30))) flush();
+    if (!tb) tb.reset(new NormTable());
+    NormTensor& T = tb->t[tb->n_tensors++];
+    T.g = G[i].data; T.n = e; T.cols = G[i].cols;
+    T.ld = has_stride(G[i]) ? G[i].ld : G[i].cols;
+    T.block_begin = (int32_t)blocks;
+    T.bf16 = G[i].dtype == SMUON_BF16;
+    T.vec = vec8(G[i]);
+    blocks += blocks_of(e);
+    by += (double)e * dtype_size(G[i].dtype);
+  }
+  flush();
+}
+
+size_t norm_ws_bytes(int32_t n_partials) { return (size_t)round_up(std::max<int64_t>(8 * (int64_t)n_partials, 256), 256); }
+
+smuon_status prepare_norm(const smuon_mat* G, int32_t n, double max_norm, float* d_out, int32_t* d_skip, void* ws,
+                          size_t ws_bytes, int32_t* d_status, NormExec* ex) {
+  smuon_status s = check_norm_tensors(G, n);
+  if (s != SMUON_OK) return s;
+  if (!d_out) return fail(SMUON_ERR_INVALID_ARG, "d_out is NULL");
+  if ((reinterpret_cast<uintptr_t>(d_out) | reinterpret_cast<uintptr_t>(d_skip) | reinterpret_cast<uintptr_t>(d_status)) % 4)
+    return fail(SMUON_ERR_INVALID_ARG, "d_out, d_skip and d_status must be 4-byte aligned");
+  if (!(max_norm > 0)) return fail(SMUON_ERR_INVALID_ARG, "max_norm=%g must be > 0", max_norm);
+  int32_t parts = 0;
+  norm_tables(G, n, reinterpret_cast<double*>(ws), &ex->tables, &ex->bytes, &parts);
+  if ((s = check_ws(ws, ws_bytes, norm_ws_bytes(parts))) != SMUON_OK) return s;
+  if ((s = device_info(&ex->di)) != SMUON_OK) return s;
+  ex->o.partials = reinterpret_cast<const double*>(ws);
+  ex->o.n_partials = parts;
+  ex->o.max_norm = max_norm;
+  ex->o.out = d_out;
+  ex->o.skip = d_skip;
+  ex->o.status = d_status;
+  return SMUON_OK;
+}
+
+smuon_status run_norm(const NormExec& ex, cudaStream_t s) {
+  for (size_t i = 0; i < ex.tables.size(); ++i) {
+    Launch L("k_grad_sumsq", SMUON_WORK_BYTES, ex.bytes[i], s);
+    CUDA_TRY(launch_grad_norm(*ex.tables[i], s));
+  }
+  Launch L("k_grad_norm_finish", SMUON_WORK_BYTES, 8.0 * ex.o.n_partials + 8, s);
+  CUDA_TRY(launch_grad_norm_finish(ex.o, s));
+  return SMUON_OK;
+}
+
+}  // namespace
+
 // plan handles: host objects holding everything needed to relaunch a call
 struct smuon_plan_s {
-  int kind;  // 0 = Newton-Schulz, 1 = update
+  int kind;  // 0 = Newton-Schulz, 1 = update, 2 = AdamW, 3 = gradient norm
   NsExec ns;
   UpdExec upd;
+  AdExec ad;
+  NormExec norm;
 };
 
 extern "C" {
@@ -1348,6 +1697,136 @@ smuon_status smuon_update_execute(smuon_plan plan, void* stream) {
 }
 
 void smuon_plan_destroy(smuon_plan plan) { delete plan; }
+
+smuon_status adamw_step(adamw_state* st, const smuon_mat* G, double lr, double beta1, double beta2, double eps,
+                        const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if, void* stream) {
+  return guarded([&]() -> smuon_status {
+    AdExec ex;
+    smuon_status s = prepare_adamw(st, G, beta1, beta2, eps, d_lr, d_grad_scale, d_skip_if, &ex);
+    if (s != SMUON_OK) return s;
+    return run_adamw(ex, st, lr, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+smuon_status adamw_plan_create(const adamw_state* st, const smuon_mat* G, double beta1, double beta2, double eps,
+                               const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if,
+                               smuon_plan* out) {
+  if (!out) return fail(SMUON_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  return guarded([&]() -> smuon_status {
+    std::unique_ptr<smuon_plan_s> p(new smuon_plan_s());
+    p->kind = 2;
+    smuon_status s = prepare_adamw(st, G, beta1, beta2, eps, d_lr, d_grad_scale, d_skip_if, &p->ad);
+    if (s != SMUON_OK) return s;
+    *out = p.release();
+    return SMUON_OK;
+  });
+}
+
+smuon_status adamw_execute(smuon_plan plan, adamw_state* st, double lr, void* stream) {
+  if (!plan || plan->kind != 2) return fail(SMUON_ERR_INVALID_ARG, "not an AdamW plan");
+  if (!st) return fail(SMUON_ERR_INVALID_ARG, "st is NULL");
+  return run_adamw(plan->ad, st, lr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* stream) {
+  return guarded([&]() -> smuon_status {
+    bool from8 = false, to8 = false;
+    smuon_status s = check_state(src, &from8);
+    if (s != SMUON_OK) return s;
+    if ((s = check_state(dst, &to8)) != SMUON_OK) return s;
+    if (from8 == to8) return fail(SMUON_ERR_DTYPE, "one state must have F32 moments and the other E4M3");
+    if (src->n_tensors != dst->n_tensors) return fail(SMUON_ERR_SHAPE, "the states have %d and %d tensors", src->n_tensors, dst->n_tensors);
+    if ((src->d_t == nullptr) != (dst->d_t == nullptr))
+      return fail(SMUON_ERR_INVALID_ARG, "both states must count their steps in one place (d_t, or t)");
+    const adamw_state* s32 = to8 ? src : dst;
+    const adamw_state* s8 = to8 ? dst : src;
+    std::vector<Span> spans;
+    std::vector<ConvTensor> ts;
+    for (int i = 0; i < src->n_tensors; ++i) {
+      const int64_t n = entries(src->W[i]);
+      if (entries(dst->W[i]) != n) return fail(SMUON_ERR_SHAPE, "tensor %d has %lld and %lld entries", i, (long long)n, (long long)entries(dst->W[i]));
+      if (!n) continue;
+      add_moments(spans, src, i, from8, false);
+      add_moments(spans, dst, i, to8, true);
+      ConvTensor T{};
+      T.m32 = s32->m[i].data; T.v32 = s32->v[i].data; T.m8 = s8->m[i].data; T.v8 = s8->v[i].data;
+      T.scales = s8->scales[i];
+      T.n = n;
+      T.vec = vec8(s32->m[i]) && vec8(s32->v[i]) && vec8(s8->m[i]) && vec8(s8->v[i]);
+      ts.push_back(T);
+    }
+    if ((s = check_overlap(spans)) != SMUON_OK) return s;
+    DevInfo di;
+    if ((s = device_info(&di)) != SMUON_OK) return s;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    std::unique_ptr<ConvTable> tb(new ConvTable());
+    for (size_t i = 0; i < ts.size();) {
+      tb->n_tensors = 0;
+      tb->to8 = to8;
+      int64_t blocks = 0;
+      double bytes = 0;
+      while (i < ts.size() && tb->n_tensors < kAdMany && blocks + blocks_of(ts[i].n) < ((int64_t)1 << 30) + 1) {
+        tb->t[tb->n_tensors] = ts[i];
+        tb->t[tb->n_tensors++].block_begin = (int32_t)blocks;
+        blocks += blocks_of(ts[i].n);
+        bytes += 10.0 * (double)ts[i].n + 2.0 * (double)blocks_of(ts[i].n);
+        ++i;
+      }
+      tb->total_blocks = (int32_t)blocks;
+      Launch L("k_adamw_convert", SMUON_WORK_BYTES, bytes, strm);
+      CUDA_TRY(launch_adamw_convert(*tb, di.sms, strm));
+    }
+    if (src->d_t && src->d_t != dst->d_t)
+      CUDA_TRY(cudaMemcpyAsync(dst->d_t, src->d_t, sizeof(int64_t), cudaMemcpyDeviceToDevice, strm));
+    dst->t = src->t;
+    return SMUON_OK;
+  });
+}
+
+smuon_status smuon_grad_norm_workspace_bytes(const smuon_mat* G, int32_t n_tensors, size_t* bytes) {
+  if (!bytes) return fail(SMUON_ERR_INVALID_ARG, "bytes is NULL");
+  return guarded([&]() -> smuon_status {
+    smuon_status s = check_norm_tensors(G, n_tensors);
+    if (s != SMUON_OK) return s;
+    std::vector<std::unique_ptr<NormTable>> tables;
+    std::vector<double> by;
+    int32_t parts = 0;
+    norm_tables(G, n_tensors, nullptr, &tables, &by, &parts);
+    *bytes = norm_ws_bytes(parts);
+    return SMUON_OK;
+  });
+}
+
+smuon_status smuon_grad_norm(const smuon_mat* G, int32_t n_tensors, double max_norm, float* d_out, int32_t* d_skip,
+                             void* ws, size_t ws_bytes, int32_t* d_status, void* stream) {
+  return guarded([&]() -> smuon_status {
+    NormExec ex;
+    smuon_status s = prepare_norm(G, n_tensors, max_norm, d_out, d_skip, ws, ws_bytes, d_status, &ex);
+    if (s != SMUON_OK) return s;
+    return run_norm(ex, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+smuon_status smuon_grad_norm_plan_create(const smuon_mat* G, int32_t n_tensors, double max_norm, float* d_out,
+                                         int32_t* d_skip, void* ws, size_t ws_bytes, int32_t* d_status,
+                                         smuon_plan* out) {
+  if (!out) return fail(SMUON_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  return guarded([&]() -> smuon_status {
+    std::unique_ptr<smuon_plan_s> p(new smuon_plan_s());
+    p->kind = 3;
+    smuon_status s = prepare_norm(G, n_tensors, max_norm, d_out, d_skip, ws, ws_bytes, d_status, &p->norm);
+    if (s != SMUON_OK) return s;
+    *out = p.release();
+    return SMUON_OK;
+  });
+}
+
+smuon_status smuon_grad_norm_execute(smuon_plan plan, void* stream) {
+  if (!plan || plan->kind != 3) return fail(SMUON_ERR_INVALID_ARG, "not a gradient-norm plan");
+  return run_norm(plan->norm, reinterpret_cast<cudaStream_t>(stream));
+}
 
 smuon_status cachemuon_workspace_bytes(const smuon_mat* M_t, size_t* bytes) {
   if (!M_t || !bytes) return fail(SMUON_ERR_INVALID_ARG, "NULL argument");

@@ -1,0 +1,99 @@
+// adamw.cuh -- tables and launchers of the AdamW kernels (k_adamw.cu), shared with the host ABI.
+#pragma once
+
+#include <stdint.h>
+
+#include "smuon.h"
+#include <cuda_runtime.h>
+
+namespace smuon {
+
+constexpr int kAdBlock = 256;  // entries per block: one warp, eight per lane; the 8-bit states' scale group
+
+// One tensor of a launch. States and master are contiguous; W and G may have a row stride.
+struct AdTensor {
+  void* w;
+  const void* g;
+  float* master;          // nullable: W's float32 original
+  void* m;                // F32, or E4M3 codes
+  void* v;                // F32, or E4M3 codes of its square root
+  uint8_t* scales;        // 8-bit states: two exponent bytes per block (m, root of v)
+  int64_t n, w_ld, g_ld;
+  int32_t cols;
+  int32_t block_begin;    // first block of this tensor in the launch
+  float lr_scale, wd;
+  uint32_t id;            // index in the call's lists: key word 1 of its rounding stream
+  int32_t flags;          // kAd*
+};
+constexpr int32_t kAdVec = 1;      // every lane's eight entries are one aligned vector in each operand
+constexpr int32_t kAdWStride = 2;  // W has a row stride
+constexpr int32_t kAdGStride = 4;
+
+// What changes from call to call, beside the table (which a plan keeps).
+struct AdHyper {
+  const int32_t* skip;    // nullable
+  const float* d_lr;      // nullable: the learning rate, else lr
+  const float* d_gscale;  // nullable: factor on the gradients
+  int64_t* d_t;           // nullable {steps taken, arrivals}: the step is d_t[0] + 1, else t
+  int64_t t;
+  double log_b1, log_b2;  // 1 - b^t = -expm1(t log b)
+  float lr, b1, c1, b2, c2, eps;
+  uint32_t seed;
+  int32_t advance;        // last launch of the call: the last CTA to read d_t[0] adds one to it
+};
+
+// Tables travel as kernel parameters (32,764 bytes at most). The small one is for calls of few tensors.
+constexpr int kAdFew = 16, kAdMany = 320;
+template <int kCap>
+struct AdTable {
+  int32_t n_tensors, total_blocks;
+  AdTensor t[kCap];
+};
+
+enum AdKind { AD_W_F32 = 0, AD_W_BF16 = 1, AD_W_MASTER = 2, AD_G_BF16 = 4, AD_8BIT = 8, AD_KINDS = 16 };
+
+template <int kCap>
+cudaError_t launch_adamw(int kind, const AdTable<kCap>& tb, const AdHyper& h, int sms, cudaStream_t s);
+
+// gradient norm: per-CTA sums of squares, then one CTA for the norm, the clip factor and the flags
+struct NormTensor {
+  const void* g;
+  int64_t n, ld;
+  int32_t cols;
+  int32_t block_begin;
+  int32_t bf16, vec;
+};
+constexpr int kNormMany = 512;
+struct NormTable {
+  int32_t n_tensors, total_blocks;
+  double* partials;
+  NormTensor t[kNormMany];
+};
+constexpr int kNormMaxGrid = 1184;
+struct NormOut {
+  const double* partials;
+  int32_t n_partials;
+  double max_norm;
+  float* out;        // {norm, factor}
+  int32_t* skip;     // nullable: 1 where the norm is not finite, else 0
+  int32_t* status;   // nullable
+};
+int norm_grid(int total_blocks);
+cudaError_t launch_grad_norm(const NormTable& tb, cudaStream_t s);
+cudaError_t launch_grad_norm_finish(const NormOut& o, cudaStream_t s);
+
+// moments from float32 to 8 bits (to8) or back; the 32-bit side may be BF16 on the way back
+struct ConvTensor {
+  void *m32, *v32, *m8, *v8;
+  uint8_t* scales;
+  int64_t n;
+  int32_t block_begin;
+  int32_t vec;
+};
+struct ConvTable {
+  int32_t n_tensors, total_blocks, to8, pad;
+  ConvTensor t[kAdMany];
+};
+cudaError_t launch_adamw_convert(const ConvTable& tb, int sms, cudaStream_t s);
+
+}  // namespace smuon

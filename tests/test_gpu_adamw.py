@@ -1,0 +1,650 @@
+"""GPU parity of the AdamW operators against the plain reference.
+
+Tolerances. The moments and the 8-bit codes have a pinned order of float32
+roundings: they are compared bit for bit. A weight W' = W - lr (wd W + u) is
+formed from those moments in float32: the direction u by two bias factors
+(expm1 of a rounded float32 argument, rsqrt), three products, one fused
+multiply-add and one division, each off by at most a few 2^-24 of itself (16 of
+them at most together: expm1 and rsqrt 2 each, their arguments and roundings 4,
+sqrt 1, the rest 5), then two fused multiply-adds and the rounding of lr. So
+|W' - exact| <= 2^-24 (2 |W'| + 20 lr (|u| + wd |W|)), plus half a bf16 step
+(2^-8 relative) where W is bf16.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import matrix_aware_sign_b200 as S
+import oracle as O
+import workloads as WL
+from matrix_aware_sign_b200 import checkpoint as C
+from oracle import adamw_oracle as A
+from tests.gpu_util import dev, host, rel_fro
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+B1, B2, EPS, LR, WD = 0.9, 0.999, 1e-8, 1e-3, 0.1
+U = 2.0 ** -24
+# one entry, below / at / above a lane's eight and a block's 256, odd matrices, several blocks
+SHAPES = [(1,), (2,), (7,), (8,), (9,), (255,), (256,), (257,), (3, 5), (17, 131), (1000,), (2, 3, 43), (64, 96), ()]
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy() if t.dtype == torch.float8_e4m3fn else t.cpu().numpy()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy().reshape(-1)
+
+
+class Reference:
+    """The run of one tensor, from float32 inputs, in the reference's arithmetic."""
+
+    def __init__(self, w, m, v, eight, index=0, seed=0, wd=WD, lr_scale=1.0, bf16=False, master=False):
+        self.w, self.m, self.v, self.eight = w.copy(), m.copy(), v.copy(), eight
+        self.index, self.seed, self.wd, self.ls, self.bf16, self.master = index, seed, wd, lr_scale, bf16, master
+        if eight:
+            self.cm, self.bm = A.encode(m)
+            self.cr, self.br = A.encode(A.f32(np.sqrt(v)))
+
+    def step(self, g, t, lr=LR, scale=None):
+        """Moves the moments; returns (exact W', tolerance)."""
+        if self.eight:
+            self.m, r = A.decode(self.cm, self.bm), A.decode(self.cr, self.br)
+            self.v = r * r
+        self.m, self.v, r = A.moments(self.m, self.v, g, B1, B2, scale)
+        u = A.direction(self.m, r, t, B1, B2, EPS)
+        lr = lr * self.ls
+        w = self.w - lr * (self.wd * self.w + u)
+        tol = U * (2 * np.abs(w) + 20 * lr * (np.abs(u) + self.wd * np.abs(self.w)))
+        if self.eight:
+            rnd = A.rounding_bits(g.size, self.index, self.seed, t)
+            self.cm, self.bm = A.encode(self.m, rnd)
+            self.cr, self.br = A.encode(r, rnd)
+        return w, tol
+
+    def check(self, opt, i, w, tol):
+        """Compares tensor i of opt, and takes over its weights (so that steps are compared one by one)."""
+        stepped = opt.master[i] if self.master else opt.W[i]
+        got = f64(stepped)
+        t = tol + (2.0 ** -8 * np.abs(w) if self.bf16 and not self.master else 0.0)
+        fine = np.isfinite(w)
+        assert np.all(np.abs(got - w)[fine] <= t[fine]), (i, np.max((np.abs(got - w) / t)[fine]))
+        assert np.array_equal(np.isfinite(got), fine)
+        if self.master:
+            assert torch.equal(opt.W[i], stepped.to(BF16))
+        if self.eight:
+            assert np.array_equal(bits(opt.m[i]).reshape(-1), self.cm)
+            assert np.array_equal(bits(opt.v[i]).reshape(-1), self.cr)
+            assert np.array_equal(opt.scales[i].cpu().numpy(), np.stack([self.bm, self.br], 1))
+        else:
+            assert np.array_equal(f64(opt.m[i]), self.m, equal_nan=True)
+            assert np.array_equal(f64(opt.v[i]), self.v, equal_nan=True)
+        self.w = got
+
+
+def draw_tensor(rng, shape, sigma=1e-3):
+    n = int(np.prod(shape, dtype=np.int64))
+    size = sigma * np.exp(rng.standard_normal(n))
+    g = rng.standard_normal(n) * size
+    m = 0.3 * rng.standard_normal(n) * size
+    v = size * size * rng.uniform(0.3, 1.3, n)
+    w = 0.02 * rng.standard_normal(n)
+    return tuple(A.f32(x) for x in (w, g, m, v))
+
+
+def make(shapes, eight, wdt, gdt, master, seed=0, t=0, rng_seed=5, **kw):
+    """(opt, G, references, gradients as the kernels see them)."""
+    rng = np.random.default_rng(seed)
+    W, G, M, V, sc, refs, gs = [], [], [], [], [], [], []
+    for i, s in enumerate(shapes):
+        w, g, m, v = draw_tensor(rng, s)
+        wt = torch.from_numpy(w.astype(np.float32)).to(wdt).cuda().reshape(s)
+        gt = torch.from_numpy(g.astype(np.float32)).to(gdt).cuda().reshape(s)
+        ref = Reference(f64(wt), m, v, eight, i, rng_seed, bf16=wdt == BF16, master=master)
+        if eight:
+            M.append(torch.from_numpy(ref.cm).cuda().view(torch.float8_e4m3fn).reshape(s))
+            V.append(torch.from_numpy(ref.cr).cuda().view(torch.float8_e4m3fn).reshape(s))
+            sc.append(torch.from_numpy(np.stack([ref.bm, ref.br], 1)).cuda())
+        else:
+            M.append(torch.from_numpy(m.astype(np.float32)).cuda().reshape(s))
+            V.append(torch.from_numpy(v.astype(np.float32)).cuda().reshape(s))
+        W.append(wt)
+        G.append(gt)
+        refs.append(ref)
+        gs.append(f64(gt))
+    opt = S.AdamW(W, m=M, v=V, scales=sc if eight else None, master=True if master else None, weight_decay=WD,
+                  seed=rng_seed, t=t, **kw)
+    return opt, G, refs, gs
+
+
+def step_refs(opt, refs, gs, t, **kw):
+    for i, (r, g) in enumerate(zip(refs, gs)):
+        r.check(opt, i, *r.step(g, t, **kw))
+
+
+# ------------------------------------------------------------------ the step
+@pytest.mark.parametrize("gdt", [F32, BF16])
+@pytest.mark.parametrize("wdt,master", [(F32, False), (BF16, False), (BF16, True)])
+@pytest.mark.parametrize("eight", [False, True])
+def test_three_steps_of_every_shape(eight, wdt, master, gdt):
+    opt, G, refs, gs = make(SHAPES, eight, wdt, gdt, master)
+    for t in (1, 2, 3):
+        S.adamw_step(opt, G, LR, B1, B2, EPS)
+        assert opt.t == t
+        step_refs(opt, refs, gs, t)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_float32_step_against_the_formula_in_64_bits(eight):
+    """Without the pinned roundings: m' = b1 m + (1-b1) g has five roundings (both factors, both products, the sum), so
+    it is within 3 U of the sum of its terms' magnitudes; v' (positive terms, one product more) within 5 U of itself."""
+    opt, G, refs, gs = make([(4099,)], eight, F32, F32, False, t=9)
+    r = refs[0]
+    m, v = r.m, r.v
+    if eight:
+        m, v = A.decode(r.cm, r.bm), A.decode(r.cr, r.br) ** 2
+    w, m64, v64 = A.step64(r.w, gs[0], m, v, 10, LR, B1, B2, EPS, WD)
+    S.adamw_step(opt, G, LR, B1, B2, EPS)
+    u = (r.w - w) / LR
+    # the direction inherits m's error, at most 3 U (|b1 m| + |c1 g|), over a root within 3 U of itself
+    root = np.sqrt(v64) / math.sqrt(1 - B2 ** 10) + EPS
+    inherited = 3 * U * (B1 * np.abs(m) + (1 - B1) * np.abs(gs[0])) / (1 - B1 ** 10) / root + 3 * U * np.abs(u)
+    assert np.all(np.abs(f64(opt.W[0]) - w) <= U * (2 * np.abs(w) + 20 * LR * (np.abs(u) + WD)) + LR * inherited)
+    if not eight:
+        assert np.all(np.abs(f64(opt.m[0]) - m64) <= 3 * U * (B1 * np.abs(m) + (1 - B1) * np.abs(gs[0])))
+        assert np.all(np.abs(f64(opt.v[0]) - v64) <= 5 * U * v64)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("t", [0, 1, 999, 10 ** 6, 2 ** 33 + 5])
+def test_late_steps(eight, t):
+    """Bias corrections and the rounding's counter (step's low word) far into a run."""
+    opt, G, refs, gs = make([(300,), (5, 7)], eight, F32, F32, False, t=t)
+    S.adamw_step(opt, G, LR, B1, B2, EPS)
+    step_refs(opt, refs, gs, t + 1)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("betas", [(0.0, 0.999), (0.9, 0.0), (0.95, 0.9999), (0.0, 0.0)])
+def test_other_betas(eight, betas):
+    opt, G, refs, gs = make([(513,)], eight, F32, F32, False, t=3)
+    S.adamw_step(opt, G, LR, *betas, EPS)
+    r, g = refs[0], gs[0]
+    m, v = (A.decode(r.cm, r.bm), A.decode(r.cr, r.br) ** 2) if eight else (r.m, r.v)
+    m, v, root = A.moments(m, v, g, *betas)
+    u = A.direction(m, root, 4, *betas, EPS)
+    w = r.w - LR * (WD * r.w + u)
+    assert np.all(np.abs(f64(opt.W[0]) - w) <= U * (2 * np.abs(w) + 20 * LR * (np.abs(u) + WD * np.abs(r.w))))
+    if eight:
+        rnd = A.rounding_bits(g.size, 0, r.seed, 4)
+        assert np.array_equal(bits(opt.m[0]), A.encode(m, rnd)[0]) and np.array_equal(bits(opt.v[0]), A.encode(root, rnd)[0])
+    else:
+        assert np.array_equal(f64(opt.m[0]), m) and np.array_equal(f64(opt.v[0]), v)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("wdt,gdt", [(F32, BF16), (BF16, F32)])
+def test_column_ranges_and_odd_addresses(eight, wdt, gdt):
+    """W and G as column ranges of wider matrices (aligned and not), moments at odd addresses: the rest of every buffer
+    stays as it was."""
+    rng = np.random.default_rng(8)
+    cases = [((33, 64), 96, 0, 32, 0), ((33, 64), 96, 8, 16, 0), ((9, 37), 41, 3, 1, 3), ((5, 64), 65, 0, 1, 1), ((1, 700), 704, 3, 4, 0)]
+    for rows_cols, ld, w_off, g_off, odd in cases:
+        r, c = rows_cols
+        w, g, m, v = draw_tensor(rng, (r, c))
+        wide = lambda off: max(ld, off + c)  # noqa: E731
+        wbuf = torch.full((r + 1, wide(w_off) + 8), 7.0, dtype=wdt, device="cuda")
+        gbuf = torch.full((r + 1, wide(g_off) + 8), 9.0, dtype=gdt, device="cuda")
+        W, G = wbuf[:r, w_off:w_off + c], gbuf[:r, g_off:g_off + c]
+        W.copy_(torch.from_numpy(w.astype(np.float32)).reshape(r, c))
+        G.copy_(torch.from_numpy(g.astype(np.float32)).reshape(r, c))
+        n, wref, gref = r * c, f64(W.contiguous()), f64(G.contiguous())
+        ref = Reference(wref, m, v, eight, 0, 2, bf16=wdt == BF16)
+        kind = torch.float8_e4m3fn if eight else F32
+        mbuf, vbuf = (torch.full((n + odd + 5,), 3.0, dtype=F32, device="cuda").to(kind) for _ in range(2))
+        M, V = (b[odd:odd + n] for b in (mbuf, vbuf))
+        if eight:
+            M.view(torch.uint8).copy_(torch.from_numpy(ref.cm))
+            V.view(torch.uint8).copy_(torch.from_numpy(ref.cr))
+        else:
+            M.copy_(torch.from_numpy(m))
+            V.copy_(torch.from_numpy(v))
+        sbuf = torch.full((-(-n // 256) + 2, 2), 77, dtype=torch.uint8, device="cuda")
+        sc = sbuf[1:-1]
+        sc.copy_(torch.from_numpy(np.stack([ref.bm, ref.br], 1)) if eight else sc)
+        opt = S.AdamW([W], m=[M.view(r, c)], v=[V.view(r, c)], scales=[sc] if eight else None, weight_decay=WD, seed=2)
+        S.adamw_step(opt, [G], LR, B1, B2, EPS)
+        ref.check(opt, 0, *ref.step(gref, 1))
+        keep = wbuf.clone()
+        keep[:r, w_off:w_off + c] = 7.0
+        assert torch.all(keep == 7.0) and torch.all(gbuf[r:] == 9.0)
+        three = torch.full((1,), 3.0, device="cuda").to(kind).float()
+        for b in (mbuf, vbuf):
+            assert torch.all(b[:odd].float() == three) and torch.all(b[odd + n:].float() == three)
+        assert torch.all(sbuf[0] == 77) and torch.all(sbuf[-1] == 77)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_two_weights_in_one_matrix(eight):
+    """Column halves of one matrix as two weights of a call."""
+    rng = np.random.default_rng(4)
+    both = dev(rng.standard_normal((24, 80)).astype(np.float32))
+    W = [both[:, :32], both[:, 32:]]
+    before = [f64(w.contiguous()) for w in W]
+    G = [dev(rng.standard_normal(w.shape).astype(np.float32)) for w in W]
+    opt = S.AdamW(W, bits=8 if eight else 32, weight_decay=WD, seed=5)
+    S.adamw_step(opt, G, LR, B1, B2, EPS)
+    for i in (0, 1):
+        ref = Reference(before[i], 0 * before[i], 0 * before[i], eight, i, 5)
+        ref.check(opt, i, *ref.step(f64(G[i]), 1))
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_many_tensors_mixed_types_and_empty_ones(eight):
+    """More tensors than a launch holds, of every combination of types, empty ones among them: each tensor keeps its own
+    place in the lists (the rounding's key), its own decay and learning-rate factor."""
+    rng = np.random.default_rng(6)
+    W, G, M, refs, gs, wd, ls = [], [], [], [], [], [], []
+    for i in range(700):
+        n = 0 if i % 50 == 7 else int(rng.integers(1, 600))
+        wdt, gdt = (F32, BF16)[int(rng.integers(2))], (F32, BF16)[int(rng.integers(2))]
+        w, g, m, v = draw_tensor(rng, (n,))
+        W.append(torch.from_numpy(w.astype(np.float32)).to(wdt).cuda())
+        G.append(torch.from_numpy(g.astype(np.float32)).to(gdt).cuda())
+        M.append(W[-1].float() if wdt == BF16 and rng.random() < 0.5 and n else None)
+        wd.append(float(np.float32(rng.uniform(0, 0.2))))
+        ls.append(float(np.float32(rng.uniform(0, 2))))
+        refs.append(Reference(f64(W[-1]), np.zeros(n), np.zeros(n), eight, i, 9, wd[-1], ls[-1], wdt == BF16, M[-1] is not None))
+        gs.append(f64(G[-1]))
+    opt = S.AdamW(W, bits=8 if eight else 32, master=M, weight_decay=wd, lr_scale=ls, seed=9, device_step=True)
+    for t in (1, 2):
+        S.adamw_step(opt, G, LR, B1, B2, EPS)
+        assert opt.d_t.tolist() == [t, 0]
+        for i, (r, g) in enumerate(zip(refs, gs)):
+            if g.size:
+                r.check(opt, i, *r.step(g, t))
+
+
+def test_only_empty_tensors():
+    w = [torch.zeros(0, device="cuda"), torch.zeros(0, 5, device="cuda")]
+    opt = S.AdamW(w, device_step=True)
+    S.adamw_step(opt, [torch.zeros_like(x) for x in w], LR)
+    assert opt.t == 1
+    host_opt = S.AdamW(w)
+    S.adamw_step(host_opt, [torch.zeros_like(x) for x in w], LR)
+    assert host_opt.t == 1
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_zero_gradients_and_moments_only_decay(eight):
+    w = torch.randn(1000, device="cuda")
+    opt = S.AdamW([w.clone()], bits=8 if eight else 32, weight_decay=WD)
+    S.adamw_step(opt, [torch.zeros(1000, device="cuda")], LR)
+    exact = f64(w) * (1 - LR * WD)
+    assert np.all(np.abs(f64(opt.W[0]) - exact) <= 3 * U * np.abs(exact))
+    assert not bits(opt.m[0]).any() and not bits(opt.v[0]).any()
+    assert eight is False or not opt.scales[0].any()
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_extreme_gradients(eight):
+    """Blocks of very large, very small and mixed gradients; moments that underflow in a block."""
+    n = 6 * 256
+    g = np.random.default_rng(1).standard_normal(n)
+    g[:256] *= 1e-30
+    g[256:512] *= 1e18
+    g[512:768] *= np.exp2(np.linspace(-60, 0, 256))
+    g[768] = 1e15
+    g[1024:1280] = 0
+    g[1030] = 1e-38
+    g = A.f32(g)
+    opt = S.AdamW([torch.zeros(n, device="cuda")], bits=8 if eight else 32, seed=1)
+    ref = Reference(np.zeros(n), np.zeros(n), np.zeros(n), eight, 0, 1, wd=0.0)
+    G = [dev(g.astype(np.float32))]
+    for t in (1, 2):
+        S.adamw_step(opt, G, LR, B1, B2, EPS)
+        w, tol = ref.step(g, t)
+        # float32's own spacing near zero (products and quotients below 2^-126) beside the relative errors
+        ref.check(opt, 0, w, tol + 2.0 ** -140)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_non_finite_gradients_stay_where_they_are(eight):
+    """A NaN or an infinity spoils its own weight and moments (8 bits: the moments of its block) and nothing else."""
+    n = 4 * 256 + 11
+    rng = np.random.default_rng(2)
+    w, g, _, _ = draw_tensor(rng, (n,))
+    g[300], g[700] = math.nan, math.inf
+    opt = S.AdamW([dev(w.astype(np.float32))], bits=8 if eight else 32, weight_decay=WD, seed=3)
+    S.adamw_step(opt, [dev(g.astype(np.float32))], LR, B1, B2, EPS)
+    bad = np.zeros(n, bool)
+    bad[[300, 700]] = True
+    got = f64(opt.W[0])
+    assert np.array_equal(np.isfinite(got), ~bad)
+    g0 = np.where(bad, 0, g)
+    m, v, r = A.moments(np.zeros(n), np.zeros(n), g0, B1, B2)
+    if eight:
+        rnd = A.rounding_bits(n, 0, 3, 1)
+        spoilt = (np.arange(n) // 256 == 1) | (np.arange(n) // 256 == 2)
+        assert opt.scales[0].cpu().numpy()[1:3].tolist() == [[255, 255]] * 2
+        for x, t in ((m, opt.m[0]), (r, opt.v[0])):
+            c, _ = A.encode(x, rnd)
+            assert np.array_equal(bits(t)[~spoilt], c[~spoilt]) and not bits(t)[spoilt].any()
+    else:
+        assert np.array_equal(f64(opt.m[0])[~bad], m[~bad]) and np.array_equal(f64(opt.v[0])[~bad], v[~bad])
+
+
+# ------------------------------------------------------------------ device-side arguments
+@pytest.mark.parametrize("eight", [False, True])
+def test_gradient_factor_and_learning_rate_from_the_device(eight):
+    opt, G, refs, gs = make([(600,), (3, 70)], eight, BF16, BF16, True, device_step=True)
+    coef, lr = torch.tensor([0.37], device="cuda"), torch.tensor([0.02], device="cuda")
+    S.adamw_step(opt, G, lr, B1, B2, EPS, grad_scale=coef)
+    lr32 = float(lr.double())
+    step_refs(opt, refs, gs, 1, lr=lr32, scale=0.37)
+    plan = S.AdamWPlan(opt, G, B1, B2, EPS, lr=lr, grad_scale=coef)
+    lr.fill_(0.005)
+    coef.fill_(2.5)
+    plan.run()
+    step_refs(opt, refs, gs, 2, lr=float(lr.double()), scale=2.5)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("device_step", [False, True])
+def test_a_skipped_step_changes_nothing(eight, device_step):
+    opt, G, refs, gs = make([(600,), (3, 70)], eight, BF16, F32, True, device_step=device_step)
+    everything = lambda: [x.clone() for k in (opt.W, opt.m, opt.v, opt.master, opt.scales or []) for x in k]  # noqa: E731
+    before = everything()
+    skip = torch.ones(1, dtype=torch.int32, device="cuda")
+    S.adamw_step(opt, G, LR, B1, B2, EPS, skip_if=skip)
+    for a, b in zip(before, everything()):
+        assert np.array_equal(bits(a), bits(b)) if a.dtype != BF16 else torch.equal(a, b)
+    assert opt.t == (0 if device_step else 1)
+    skip.zero_()
+    S.adamw_step(opt, G, LR, B1, B2, EPS, skip_if=skip)
+    step_refs(opt, refs, gs, 1 if device_step else 2)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_captured_steps_count_on(eight):
+    """A step captured once and replayed equals the same number of eager steps, bit for bit; a plan's first run may be
+    the captured one."""
+    a = make([(700,), (33, 40), (1,)], eight, BF16, BF16, True, device_step=True)
+    b = make([(700,), (33, 40), (1,)], eight, BF16, BF16, True, device_step=True)
+    lr = torch.tensor([LR], device="cuda")
+    plan = S.AdamWPlan(a[0], a[1], B1, B2, EPS, lr=lr)
+    norm = S.GradNorm(a[1], 0.01)
+    clipped = S.AdamWPlan(a[0], a[1], B1, B2, EPS, lr=lr, grad_scale=norm.coef, skip_if=norm.skip)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.run()
+        norm.run()
+        clipped.run()
+    out, skip = torch.zeros(2, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        graph.replay()
+        S.adamw_step(b[0], b[1], lr, B1, B2, EPS)
+        ws = S.smuon_grad_norm(b[1], 0.01, out, skip)
+        S.adamw_step(b[0], b[1], lr, B1, B2, EPS, grad_scale=out[1:], skip_if=skip)
+        torch.cuda.synchronize()
+        del ws
+    assert a[0].t == b[0].t == 6
+    for k in ("W", "m", "v", "master", "scales"):
+        for x, y in zip(getattr(a[0], k) or [], getattr(b[0], k) or []):
+            assert torch.equal(x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x,
+                               y.view(torch.uint8) if y.dtype == torch.float8_e4m3fn else y)
+    assert torch.equal(norm.out, out)
+
+
+def test_steps_on_another_stream():
+    opt, G, refs, gs = make([(70000,), (33, 40)], True, F32, F32, False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        S.adamw_step(opt, G, LR, B1, B2, EPS)
+    S.adamw_step(opt, G, LR, B1, B2, EPS, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for i, (r, g) in enumerate(zip(refs, gs)):
+        w, tol = r.step(g, 1)
+        r.w = w
+        w2, tol2 = r.step(g, 2)
+        r.check(opt, i, w2, tol + tol2 + U * np.abs(w2))
+
+
+def test_results_do_not_depend_on_the_split():
+    """The same tensors in one call, one by one in calls of their own (32 bits), and prepared: equal bits."""
+    shapes = [(257,), (40, 41), (3000,)]
+    a, b, c = (make(shapes, False, F32, F32, False) for _ in range(3))
+    S.adamw_step(a[0], a[1], LR, B1, B2, EPS)
+    S.AdamWPlan(b[0], b[1], B1, B2, EPS).run(LR)
+    for i in range(3):
+        one = S.AdamW([c[0].W[i]], m=[c[0].m[i]], v=[c[0].v[i]], weight_decay=WD)
+        S.adamw_step(one, [c[1][i]], LR, B1, B2, EPS)
+    for other in (b, c):
+        for k in ("W", "m", "v"):
+            assert all(torch.equal(x, y) for x, y in zip(getattr(a[0], k), getattr(other[0], k)))
+
+
+# ------------------------------------------------------------------ conversion
+def test_convert_both_ways():
+    shapes = SHAPES + [(0,), (70001,)]
+    opt32, _, refs, _ = make(shapes, False, F32, F32, False, t=41)
+    opt32.m[-1][5], opt32.v[-1][600] = math.nan, math.inf
+    opt8 = S.AdamW([w.clone() for w in opt32.W], bits=8)
+    S.adamw_convert(opt32, opt8)
+    assert opt8.t == 41
+    for i in range(len(shapes)):
+        for x, codes, col in ((f64(opt32.m[i]), opt8.m[i], 0), (A.f32(np.sqrt(f64(opt32.v[i]))), opt8.v[i], 1)):
+            c, b = A.encode(x)
+            assert np.array_equal(bits(codes).reshape(-1), c) and np.array_equal(opt8.scales[i].cpu().numpy()[:, col], b)
+    back = S.AdamW([w.clone() for w in opt32.W])
+    S.adamw_convert(opt8, back)
+    for i in range(len(shapes)):
+        sc = opt8.scales[i].cpu().numpy()
+        m, r = A.decode(bits(opt8.m[i]).reshape(-1), sc[:, 0]), A.decode(bits(opt8.v[i]).reshape(-1), sc[:, 1])
+        assert np.array_equal(f64(back.m[i]), m, equal_nan=True)
+        assert np.array_equal(f64(back.v[i]), A.f32(r * r), equal_nan=True)
+    again = S.AdamW([w.clone() for w in opt32.W], bits=8)
+    S.adamw_convert(back, again)
+    # What 8 bits hold converts to the same values (v's root is exact), though not always to the same codes: a block's
+    # largest y in [248, 256) rounds to 256, so the second conversion takes the next exponent for the block. There every
+    # value of at least 2^-6 units still has its three mantissa bits; smaller ones are rounded to its 2^-9 units again.
+    for i in range(len(shapes)):
+        s1, s2 = opt8.scales[i].cpu().numpy(), again.scales[i].cpu().numpy()
+        for c1, c2, col in ((opt8.m[i], again.m[i], 0), (opt8.v[i], again.v[i], 1)):
+            x, y = A.decode(bits(c1).reshape(-1), s1[:, col]), A.decode(bits(c2).reshape(-1), s2[:, col])
+            unit = np.repeat(np.exp2(s2[:, col].astype(float) - 127), 256)[:x.size]
+            large = np.abs(x) >= 2.0 ** -6 * unit
+            assert np.array_equal(np.isnan(x), np.isnan(y)) and np.array_equal(x[large], y[large])
+            small = ~large & ~np.isnan(x)
+            assert np.all(np.abs(x - y)[small] <= 2.0 ** -10 * unit[small])
+
+
+def test_convert_at_odd_addresses_and_counts():
+    n = 777
+    m, v = torch.randn(n + 3, device="cuda")[3:], torch.rand(n + 1, device="cuda")[1:]
+    w = torch.zeros(n, device="cuda")
+    src = S.AdamW([w], m=[m], v=[v], t=7, device_step=True)
+    cm, cv = (torch.zeros(n + 7, dtype=torch.uint8, device="cuda") for _ in range(2))
+    dst = S.AdamW([w], m=[cm[3:n + 3].view(torch.float8_e4m3fn)], v=[cv[1:n + 1].view(torch.float8_e4m3fn)],
+                  scales=[torch.zeros(4, 2, dtype=torch.uint8, device="cuda")], device_step=True)
+    S.adamw_convert(src, dst)
+    assert dst.t == 7
+    assert np.array_equal(cm[3:n + 3].cpu().numpy(), A.encode(f64(m))[0])
+    assert np.array_equal(cv[1:n + 1].cpu().numpy(), A.encode(A.f32(np.sqrt(f64(v))))[0])
+    assert not cm[:3].any() and not cm[n + 3:].any() and not cv[:1].any() and not cv[n + 1:].any()
+
+
+# ------------------------------------------------------------------ gradient norm
+def norm_of(G, max_norm, **kw):
+    out = torch.full((2,), -1.0, device="cuda")
+    skip = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    S.smuon_grad_norm(G, max_norm, out, skip, status=status, **kw)
+    torch.cuda.synchronize()
+    return float(out[0]), float(out[1]), int(skip), int(status)
+
+
+def check_norm(G, max_norm):
+    """Eight squares by fused multiply-adds: 8 roundings of at most U each on positive terms, so the sum is within 8 U and
+    its root within 4 U; one rounding of the result (half a step: U, or 2^-150 below 2^-126, where float32's numbers are
+    2^-149 apart) and of the factor."""
+    want, coef = A.grad_norm([f64(g.contiguous()) for g in G], max_norm)
+    got, c, skip, status = norm_of(G, max_norm)
+    assert abs(got - want) <= 6 * U * want + 2.0 ** -150 and abs(c - coef) <= 6 * U * coef, (got, want)
+    assert skip == 0 and status == 0
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 255, 256, 257, 2049, 70001, 3_000_001])
+def test_norm_of_one_tensor(n, dt):
+    G = [torch.randn(n, device="cuda").to(dt)]
+    for max_norm in (1e-3, 1e9, math.inf):
+        check_norm(G, max_norm)
+
+
+def test_norm_of_many_tensors_with_strides():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    G = []
+    for i in range(1100):
+        n = 0 if i == 50 else int(torch.randint(1, 900, (1,)).item())
+        G.append(torch.randn(n, device="cuda", generator=g).to(BF16 if i % 3 else F32))
+    big = torch.randn(65, 129, device="cuda", generator=g)
+    G += [big[:, 1:38], torch.randn(64, 128, device="cuda", generator=g)[:, 64:], torch.randn(12, 10, device="cuda").to(BF16)[:, 1:2],
+          torch.randn(1001, device="cuda", generator=g)[1:]]
+    check_norm(G, 1.0)
+
+
+@pytest.mark.parametrize("size", [1e-42, 1e-30, 1e-22, 1e17, 1e19, 1e30])
+def test_norm_of_small_and_large_gradients(size):
+    """Squares beyond float32's range, up and down; one of ordinary size would drown them, so they are alone. The
+    smallest are subnormal float32 numbers (exact in float64)."""
+    x = (np.random.default_rng(0).standard_normal(5000) * size).astype(np.float32)
+    check_norm([dev(x)], size)
+    check_norm([torch.cat([dev(x), torch.zeros(300, device="cuda")])], size)
+
+
+def test_norm_of_nothing_and_of_zeros():
+    assert norm_of([torch.zeros(0, device="cuda")], 1.0)[:3] == (0.0, 1.0, 0)
+    assert norm_of([torch.zeros(5000, device="cuda")], 1.0)[:3] == (0.0, 1.0, 0)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 3e38])
+def test_norm_that_float32_does_not_hold(bad):
+    G = [torch.randn(3000, device="cuda"), torch.full((3000,), 1.0, device="cuda")]
+    G[1][1234] = bad
+    if bad == 3e38:
+        G[1][1235] = 3e38
+    norm, coef, skip, status = norm_of(G, 1.0)
+    assert coef == 0.0 and skip == 1 and status == S.DEV_NONFINITE_NORM
+    assert math.isnan(norm) if math.isnan(bad) else norm == math.inf
+
+
+def test_norm_is_the_same_every_time():
+    G = [torch.randn(n, device="cuda") for n in (1_000_003, 17, 65536)]
+    a = S.GradNorm(G, 1.0)
+    a.run()
+    first = a.out.clone()
+    for _ in range(5):
+        a.run()
+        assert torch.equal(a.out, first)
+    out = torch.zeros(2, device="cuda")
+    S.smuon_grad_norm(G, 1.0, out)
+    assert torch.equal(out, first)
+
+
+# ------------------------------------------------------------------ a run of them together
+@pytest.mark.parametrize("eight", [False, True])
+def test_training_steps_beside_sign_muon(eight):
+    """Matrices by Sign-Muon, the other parameters by a clipped AdamW step, one of the steps with a gradient that is not
+    finite: it is skipped, the others follow the reference; stopped and resumed, the run goes on bit for bit."""
+    rng = np.random.default_rng(12)
+    mats, others = [(64, 96), (128, 64)], [(500, 64), (64,), (64,), (192,)]
+    Wm = [dev(0.02 * rng.standard_normal(s).astype(np.float32)) for s in mats]
+    mom = [torch.zeros(s, device="cuda") for s in mats]
+    Um = [torch.zeros(s, dtype=BF16, device="cuda") for s in mats]
+    Gm = [torch.zeros(s, device="cuda") for s in mats]
+    wm_ref = [host(w).astype(np.float64) for w in Wm]
+    mom_ref = [np.zeros(s) for s in mats]
+    Wo = [dev((0.02 * rng.standard_normal(s)).astype(np.float32)).to(BF16) for s in others]
+    Go = [torch.zeros(s, dtype=BF16, device="cuda") for s in others]
+    opt = S.AdamW(Wo, bits=8 if eight else 32, master=True, weight_decay=[WD, 0.0, 0.0, 0.0], seed=21, device_step=True)
+    refs = [Reference(f64(opt.master[i]), 0 * f64(w), 0 * f64(w), eight, i, 21, WD if i == 0 else 0.0, bf16=True, master=True)
+            for i, w in enumerate(Wo)]
+    norm = S.GradNorm(Go, 0.5)
+    plan = S.AdamWPlan(opt, Go, B1, B2, EPS, grad_scale=norm.coef, skip_if=norm.skip)
+    ns = S.NsPlan(mom, Um, *WL.QUINTIC, 5, G=Gm, beta=0.9, flags=S.NS_SPLIT_BF16)
+    upd = S.UpdatePlan(Wm, 0.01, U=[[u] for u in Um], M=1)
+    saved, t = None, 0
+    for step in range(5):
+        gm = [rng.standard_normal(s).astype(np.float32) for s in mats]
+        go = [torch.from_numpy((0.1 * rng.standard_normal(s)).astype(np.float32)).to(BF16) for s in others]
+        if step == 2:
+            go[1][3] = math.nan
+        for d, s in zip(Gm + Go, [torch.from_numpy(x) for x in gm] + go):
+            d.copy_(s)
+        ns.run()
+        upd.run()
+        norm.run()
+        plan.run(LR)
+        for i in range(len(mats)):
+            mom_ref[i] = 0.9 * mom_ref[i] + gm[i]
+            u = O.newton_schulz(mom_ref[i], *WL.QUINTIC, 5)
+            assert rel_fro(host(Um[i]), u) < 1e-2
+            wm_ref[i] = wm_ref[i] - 0.01 * O.sign_extract(host(Um[i]))
+            np.testing.assert_allclose(host(Wm[i]), wm_ref[i], atol=(step + 1) * 2.0 ** -24)
+        if step == 2:
+            assert int(norm.skip) == 1
+            continue
+        t += 1
+        want, coef = A.grad_norm([f64(g) for g in go], 0.5)
+        assert abs(float(norm.norm) - want) <= 6 * U * want and abs(float(norm.coef) - coef) <= 6 * U * coef
+        step_refs(opt, refs, [f64(g) for g in go], t, scale=float(norm.coef.double()))
+        if step == 1:
+            saved = C.snapshot(opt)
+    assert opt.t == t == 4
+    # resumed from the second step's snapshot in fresh buffers with the same gradients
+    fresh = S.AdamW([torch.zeros_like(w) for w in Wo], bits=8 if eight else 32, master=True,
+                    weight_decay=[WD, 0.0, 0.0, 0.0], seed=21, device_step=True)
+    C.restore(fresh, saved)
+    a, b = S.AdamW([w.clone() for w in Wo], bits=8 if eight else 32, master=True, weight_decay=[WD, 0.0, 0.0, 0.0],
+                   seed=21, device_step=True), fresh
+    C.restore(a, saved)
+    for _ in range(2):
+        S.adamw_step(a, Go, LR, B1, B2, EPS)
+        S.AdamWPlan(b, Go, B1, B2, EPS).run(LR)
+    assert a.t == b.t == 4
+    for k in ("W", "m", "v", "master", "scales"):
+        for x, y in zip(getattr(a, k) or [], getattr(b, k) or []):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_binding_refuses_what_is_not_one_device_or_one_value():
+    w = [torch.zeros(8, device="cuda")]
+    opt = S.AdamW(w)
+    with pytest.raises(ValueError, match="CUDA device"):
+        S.adamw_step(opt, [torch.zeros(8)], LR)
+    with pytest.raises(ValueError, match="shape"):
+        S.adamw_step(opt, [torch.zeros(4, 2, device="cuda")], LR)
+    with pytest.raises(ValueError):
+        S.adamw_step(opt, [torch.zeros(8, device="cuda")] * 2, LR)
+    with pytest.raises(ValueError, match="grad_scale"):
+        S.adamw_step(opt, [torch.zeros(8, device="cuda")], LR, grad_scale=torch.ones(2, device="cuda"))
+    with pytest.raises(ValueError, match="skip_if"):
+        S.adamw_step(opt, [torch.zeros(8, device="cuda")], LR, skip_if=torch.ones(1, device="cuda"))
+    with pytest.raises(S.SmuonError, match="lr"):
+        S.adamw_step(opt, [torch.zeros(8, device="cuda")], -1.0)
+    with pytest.raises(S.SmuonError, match="lr"):
+        S.adamw_step(opt, [torch.zeros(8, device="cuda")], math.nan)
+    with pytest.raises(S.SmuonError, match="overlap"):
+        S.adamw_step(opt, [w[0]], LR)
+    with pytest.raises(S.SmuonError, match="overlap"):
+        S.adamw_step(S.AdamW([w[0], w[0]]), [torch.zeros(8, device="cuda")] * 2, LR)
+    plan = S.AdamWPlan(opt, [torch.zeros(8, device="cuda")])
+    with pytest.raises(ValueError, match="lr"):
+        plan.run()
+    assert opt.t == 0 and not w[0].any()
