@@ -1518,7 +1518,12 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
   h.b1 = (float)beta1; h.c1 = (float)(1.0 - beta1);
   h.b2 = (float)beta2; h.c2 = (float)(1.0 - beta2);
   h.eps = (float)eps;
+  h.one2 = make_float2(1.f, 1.f);
+  h.c1_2 = make_float2(h.c1, h.c1);
+  h.c2_2 = make_float2(h.c2, h.c2);
+  h.eps2 = make_float2(h.eps, h.eps);
   h.seed = st->seed;
+  for (int r = 0; r < 10; ++r) h.k0[r] = st->seed + (uint32_t)r * 0x9E3779B9u;
   return SMUON_OK;
 }
 

@@ -38,7 +38,9 @@ struct AdHyper {
   int64_t t;
   double log_b1, log_b2;  // 1 - b^t = -expm1(t log b)
   float lr, b1, c1, b2, c2, eps;
-  uint32_t seed;
+  float2 one2, c1_2, c2_2, eps2;  // both halves alike: operands of the packed operations
+  uint32_t seed;          // key word 0 of the rounding stream, and its ten rounds' values
+  uint32_t k0[10];
   int32_t advance;        // last launch of the call: the last CTA to read d_t[0] adds one to it
 };
 

@@ -39,13 +39,19 @@ __device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(u[k]);
 }
+// bf16 halves to float32 by the mixed-precision add, which leaves the integer pipe to the codes and random bits
+__device__ __forceinline__ float add_bf16(uint16_t a) {
+  float d;
+  asm("add.f32.bf16 %0, %1, %2;" : "=f"(d) : "h"(a), "f"(-0.f));
+  return d;
+}
 __device__ __forceinline__ void ld8(const __nv_bfloat16* p, float (&x)[8]) {
   const uint4 w = *reinterpret_cast<const uint4*>(p);
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __uint_as_float(u[k] << 16);
-    x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    x[2 * k] = add_bf16((uint16_t)u[k]);
+    x[2 * k + 1] = add_bf16((uint16_t)(u[k] >> 16));
   }
 }
 __device__ __forceinline__ void st8(float* p, const float (&x)[8]) {
@@ -114,6 +120,10 @@ __device__ __forceinline__ void decode8(const uint2 c, float scale, float (&x)[8
   }
 }
 
+__device__ __forceinline__ float decode1(uint8_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
+}
+
 __device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t e0, int64_t n, bool vec) {
   if (vec) return *reinterpret_cast<const uint2*>(p + e0);
   uint32_t w[2] = {0, 0};
@@ -165,35 +175,303 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte, con
   return make_uint2(out[0], out[1]);
 }
 
-// last tensor whose first block is at or before b; monotonic from `li` on
+// last tensor whose first block is at or before b; li: one known to begin at or before b
 template <class Table>
 __device__ __forceinline__ int tensor_of(const Table& tb, int b, int li) {
-  if (li < 0) {
-    int lo = 0, hi = tb.n_tensors - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (tb.t[mid].block_begin <= b) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+  int lo = li, hi = tb.n_tensors - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tb.t[mid].block_begin <= b) lo = mid; else hi = mid - 1;
   }
-  while (li + 1 < tb.n_tensors && tb.t[li + 1].block_begin <= b) ++li;
-  return li;
+  return lo;
+}
+
+// ---------------------------------------------------------------- the step
+// per-call numbers, the same for every entry
+struct Consts {
+  float b1, c1, b2, c2, eps, gs, lr, ic1, ic2;  // ic1 = 1 / (1 - b1^t), ic2 = 1 / sqrt(1 - b2^t)
+  uint32_t t, seed;
+};
+
+template <int kKind>
+struct Kind {
+  static constexpr bool master = (kKind & 3) == AD_W_MASTER, eight = (kKind & AD_8BIT) != 0;
+  using W = typename std::conditional<(kKind & 3) == AD_W_F32, float, __nv_bfloat16>::type;
+  using G = typename std::conditional<(kKind & AD_G_BF16) != 0, __nv_bfloat16, float>::type;
+};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+
+// W' from m' and r' = sqrt(v'); square root and reciprocal are approximations within two units in the last place:
+// the direction is rounded to 2^-24 of W afterwards, which it is a small part of
+__device__ __forceinline__ float weight_step(float w, float m, float r, float decay, float step, const Consts& c) {
+  return fmaf(-step, m * rcp_approx(fmaf(r, c.ic2, c.eps)), fmaf(-decay, w, w));  // step = lr / (1 - b1^t), decay = lr wd
+}
+
+__device__ __forceinline__ float sqrt_approx(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Any block: short ones, operands off their vector addresses, row strides that are no multiple of eight, 8-bit blocks
+// whose scales leave the range of the fast form or whose values are not finite. Entry by entry; with float32 moments
+// the lanes' entries lie side by side, so the accesses coalesce.
+template <int kKind>
+__device__ __noinline__ void step_block_any(const AdTensor& T, int64_t blk, int lane, const Consts& c) {
+  using K = Kind<kKind>;
+  using WT = typename K::W;
+  using GT = typename K::G;
+  const int64_t n = T.n;
+  const bool ws = T.flags & kAdWStride, gst = T.flags & kAdGStride;
+  const float lr = c.lr * T.lr_scale, step = lr * c.ic1, decay = lr * T.wd;
+  const uint32_t sc = K::eight ? *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk) : 0u;
+  float m8[8], r8[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t e = blk * kAdBlock + (K::eight ? lane * 8 + k : lane + 32 * k);
+    float m = 0.f, r = 0.f;
+    if (e < n) {
+      const int64_t wo = ws ? strided(e, T.cols, T.w_ld) : e, go = gst ? strided(e, T.cols, T.g_ld) : e;
+      float v;
+      if (K::eight) {
+        m = __fmul_rn(decode1(reinterpret_cast<const uint8_t*>(T.m)[e]), scale_of(sc & 255u));
+        v = __fmul_rn(decode1(reinterpret_cast<const uint8_t*>(T.v)[e]), scale_of(sc >> 8));
+        v = __fmul_rn(v, v);
+      } else {
+        m = reinterpret_cast<const float*>(T.m)[e];
+        v = reinterpret_cast<const float*>(T.v)[e];
+      }
+      const float g = __fmul_rn(c.gs, to_f32(reinterpret_cast<const GT*>(T.g)[go]));
+      m = __fadd_rn(__fmul_rn(c.b1, m), __fmul_rn(c.c1, g));
+      v = __fadd_rn(__fmul_rn(c.b2, v), __fmul_rn(c.c2, __fmul_rn(g, g)));
+      r = __fsqrt_rn(v);
+      WT* w = reinterpret_cast<WT*>(T.w) + wo;
+      const float x = weight_step(K::master ? T.master[e] : to_f32(*w), m, r, decay, step, c);
+      if (K::master) T.master[e] = x;
+      put(w, x);
+      if (!K::eight) {
+        reinterpret_cast<float*>(T.m)[e] = m;
+        reinterpret_cast<float*>(T.v)[e] = v;
+      }
+    }
+    m8[k] = m;  // zero past a short last block
+    r8[k] = r;
+  }
+  if (K::eight) {
+    const int64_t e0 = blk * kAdBlock + lane * 8;
+    const uint32_t bm = block_exponent(m8), br = block_exponent(r8);
+    const uint64_t grp = (uint64_t)e0 >> 3;
+    const uint4 rnd = crng::philox4x32_10(make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), c.t, 1u), c.seed, T.id);
+    store_codes(reinterpret_cast<uint8_t*>(T.m), e0, n, false, encode8<true>(m8, bm, rnd));
+    store_codes(reinterpret_cast<uint8_t*>(T.v), e0, n, false, encode8<true>(r8, br, rnd));
+    if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
+  }
+}
+
+// A whole block with vector operands, float32 moments.
+template <int kKind>
+__device__ __forceinline__ void step_block32(const AdTensor& T, int64_t blk, int lane, const Consts& c) {
+  using K = Kind<kKind>;
+  using WT = typename K::W;
+  using GT = typename K::G;
+  const int64_t e0 = blk * kAdBlock + lane * 8;
+  const int64_t wo = T.flags & kAdWStride ? strided(e0, T.cols, T.w_ld) : e0;
+  const int64_t go = T.flags & kAdGStride ? strided(e0, T.cols, T.g_ld) : e0;
+  float g[8], w[8], m[8], v[8];
+  ld8(reinterpret_cast<const GT*>(T.g) + go, g);
+  if (K::master) ld8(T.master + e0, w);
+  else ld8(reinterpret_cast<const WT*>(T.w) + wo, w);
+  ld8(reinterpret_cast<const float*>(T.m) + e0, m);
+  ld8(reinterpret_cast<const float*>(T.v) + e0, v);
+  const float lr = c.lr * T.lr_scale, step = lr * c.ic1, decay = lr * T.wd;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    g[k] = __fmul_rn(c.gs, g[k]);
+    m[k] = __fadd_rn(__fmul_rn(c.b1, m[k]), __fmul_rn(c.c1, g[k]));
+    v[k] = __fadd_rn(__fmul_rn(c.b2, v[k]), __fmul_rn(c.c2, __fmul_rn(g[k], g[k])));
+    w[k] = weight_step(w[k], m[k], __fsqrt_rn(v[k]), decay, step, c);
+  }
+  if (K::master) st8(T.master + e0, w);
+  st8(reinterpret_cast<WT*>(T.w) + wo, w);
+  st8(reinterpret_cast<float*>(T.m) + e0, m);
+  st8(reinterpret_cast<float*>(T.v) + e0, v);
+}
+
+// two float32 numbers in one register pair: one instruction for both, each rounded on its own as ever
+struct F2 {
+  unsigned long long x;
+};
+__device__ __forceinline__ F2 two(float a, float b) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d.x) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ F2 both(float a) { return two(a, a); }
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.x));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.x) : "l"(a.x), "l"(b.x));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.x) : "l"(a.x), "l"(b.x), "l"(c.x));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.x) : "l"(a.x), "l"(b.x));
+  return d;
+}
+// a + b as a 1 + b, with a one that the assembler does not know to be one: it contracts mul.rn.f32x2 and add.rn.f32x2
+// into a single rounding (with -fmad=false, too), and the moments need both
+__device__ __forceinline__ F2 add2(F2 a, F2 b, float2 one) { return fma2(a, two(one.x, one.y), b); }
+// eight codes to their values (no scale); two float32 patterns to two codes in the low half
+__device__ __forceinline__ void unpack_codes(const uint2 c, float (&x)[8]) {
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x[2 * k] = f.x;
+    x[2 * k + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint32_t codes_of(uint32_t lo, uint32_t hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  return d;
+}
+// largest magnitude of eight; NaN if one is
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max_abs8(const float (&x)[8]) {
+  return max_abs3(max_abs3(max_abs3(x[0], x[1], x[2]), x[3], x[4]), max_abs3(x[5], x[6], x[7]), 0.f);
+}
+
+// random words of a group of eight entries: Philox4x32-10 with the seed's key schedule from the parameters
+__device__ __forceinline__ uint4 group_words(int64_t e0, const Consts& c, const uint32_t (&k0)[10], uint32_t k1) {
+  const uint64_t grp = (uint64_t)e0 >> 3;
+  uint4 x = make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), c.t, 1u);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    if (r) k1 += 0xBB67AE85u;
+    const uint64_t p0 = (uint64_t)x.x * 0xD2511F53u, p1 = (uint64_t)x.z * 0xCD9E8D57u;
+    x = make_uint4((uint32_t)(p1 >> 32) ^ x.y ^ k0[r], (uint32_t)p1, (uint32_t)(p0 >> 32) ^ x.w ^ k1, (uint32_t)p0);
+  }
+  return x;
+}
+
+// A whole block with vector operands, 8-bit moments: the same values as step_block_any with fewer instructions, which
+// are what bounds it.
+//  - b1 m = (b1 2^k) code and b2 v = (b2 2^2k) code^2: a power of two commutes with the rounding, so the factor is
+//    formed once a block (while it is a normal number).
+//  - r' only goes into W' and into its code, which depends on r' through the carry out of its 20 low bits. An
+//    approximate root, made smaller by 2^-21 of itself, is below r' by less than 16 units in the last place and gives
+//    the same code unless those bits are within 16 of a carry: the warp then (one block in 250) takes exact roots. The
+//    block's exponent comes from the exact root of the largest v' (rounding is monotonic).
+// false where a value leaves the range in which this holds (nothing is written then).
+template <int kKind>
+__device__ __forceinline__ bool step_block8(const AdTensor& T, int64_t blk, int lane, const Consts& c,
+                                            const AdHyper& h) {
+  using K = Kind<kKind>;
+  using WT = typename K::W;
+  using GT = typename K::G;
+  const int64_t e0 = blk * kAdBlock + lane * 8;
+  const int64_t wo = T.flags & kAdWStride ? strided(e0, T.cols, T.w_ld) : e0;
+  const int64_t go = T.flags & kAdGStride ? strided(e0, T.cols, T.g_ld) : e0;
+  float m[8], v[8], w[8];
+  {
+    float g[8];
+    const uint32_t sc = *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk);
+    const uint2 cm = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(T.m) + e0);
+    const uint2 cr = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(T.v) + e0);
+    ld8(reinterpret_cast<const GT*>(T.g) + go, g);
+    if (K::master) ld8(T.master + e0, w);
+    else ld8(reinterpret_cast<const WT*>(T.w) + wo, w);
+    const float sm = scale_of(sc & 255u), sr = scale_of(sc >> 8);
+    const float b1s = c.b1 * sm, b2s = c.b2 * (sr * sr);
+    // exact factors: zero, or normal with room on both sides
+    if (!((sm == 0.f || (b1s >= 0x1p-100f && b1s <= 0x1p100f)) && (sr == 0.f || (b2s >= 0x1p-100f && b2s <= 0x1p100f))))
+      return false;
+    unpack_codes(cm, m);
+    unpack_codes(cr, v);
+    const F2 gs = both(c.gs), b1 = both(b1s), c1 = two(h.c1_2.x, h.c1_2.y), b2 = both(b2s), c2 = two(h.c2_2.x, h.c2_2.y);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const F2 g2 = mul2(gs, two(g[k], g[k + 1])), v2 = two(v[k], v[k + 1]);
+      split(add2(mul2(b1, two(m[k], m[k + 1])), mul2(c1, g2), h.one2), m[k], m[k + 1]);
+      split(add2(mul2(b2, mul2(v2, v2)), mul2(c2, mul2(g2, g2)), h.one2), v[k], v[k + 1]);
+    }
+  }
+  const float tm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m))));
+  const float tv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v))));
+  // finite, and so large (or zero) that the smallest v' which the root does not flush to zero is far below the codes
+  if (!(tm <= 0x1p120f && tv <= 0x1p120f && (tv == 0.f || tv >= 0x1p-80f))) return false;
+  const uint32_t fm = __float_as_uint(tm) >> 23, fr = __float_as_uint(__fsqrt_rn(tv)) >> 23;
+  const uint32_t bm = fm > 7u ? fm - 7u : 0u, br = fr > 7u ? fr - 7u : 0u;
+  const F2 um = both(bm ? __uint_as_float((254u - bm) << 23) : 0.f);
+  const F2 ur = both(br ? __uint_as_float(((254u - br) << 23) - 8u) : 0.f);  // (1 - 2^-21) 2^j
+  const uint4 rnd = group_words(e0, c, h.k0, T.id);
+  const uint32_t rw[4] = {rnd.x, rnd.y, rnd.z, rnd.w};
+  const float lr = c.lr * T.lr_scale;
+  const F2 step = both(-lr * c.ic1), decay = both(-lr * T.wd), ic2 = both(c.ic2), eps = two(h.eps2.x, h.eps2.y);
+  uint32_t om[2], orr[2], near = 0xffffffffu;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const F2 m2 = two(m[k], m[k + 1]), r2 = two(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), w2 = two(w[k], w[k + 1]);
+    float d0, d1, a0, a1, b0, b1;
+    split(fma2(r2, ic2, eps), d0, d1);
+    split(fma2(step, mul2(m2, two(rcp_approx(d0), rcp_approx(d1))), fma2(decay, w2, w2)), w[k], w[k + 1]);
+    split(mul2(m2, um), a0, a1);
+    split(mul2(r2, ur), b0, b1);
+    const uint32_t h0 = __byte_perm(rw[k >> 1], 0, 0x4410), h1 = __byte_perm(rw[k >> 1], 0, 0x4432);
+    const uint32_t pa0 = h0 * 16u + __float_as_uint(a0), pa1 = h1 * 16u + __float_as_uint(a1);
+    const uint32_t pb0 = h0 * 16u + __float_as_uint(b0), pb1 = h1 * 16u + __float_as_uint(b1);
+    near = min(near, min(~pb0 & 0xffff0u, ~pb1 & 0xffff0u));
+    const uint32_t a = codes_of(pa0 & 0xfff00000u, pa1 & 0xfff00000u), b = codes_of(pb0 & 0xfff00000u, pb1 & 0xfff00000u);
+    om[k >> 2] = k & 2 ? __byte_perm(om[k >> 2], a, 0x5410) : a;
+    orr[k >> 2] = k & 2 ? __byte_perm(orr[k >> 2], b, 0x5410) : b;
+  }
+  uint2 codes_r = make_uint2(orr[0], orr[1]);
+  if (__any_sync(0xffffffffu, near == 0u)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __fsqrt_rn(v[k]);
+    codes_r = encode8<true>(v, br, rnd);
+  }
+  if (K::master) st8(T.master + e0, w);
+  st8(reinterpret_cast<WT*>(T.w) + wo, w);
+  *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(T.m) + e0) = make_uint2(om[0], om[1]);
+  *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(T.v) + e0) = codes_r;
+  if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
+  return true;
 }
 
 }  // namespace
 
-// ---------------------------------------------------------------- the step
 template <int kKind, int kCap>
-__global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ AdTable<kCap> tb, const __grid_constant__ AdHyper h) {
-  constexpr bool kMaster = (kKind & 3) == AD_W_MASTER, k8 = (kKind & AD_8BIT) != 0;
-  using WT = typename std::conditional<(kKind & 3) == AD_W_F32, float, __nv_bfloat16>::type;
-  using GT = typename std::conditional<(kKind & AD_G_BF16) != 0, __nv_bfloat16, float>::type;
+__global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdTable<kCap> tb, const __grid_constant__ AdHyper h) {
   if (h.skip && *h.skip) return;
   const int64_t t = h.d_t ? *h.d_t + 1 : h.t;
-  const float lr = h.d_lr ? *h.d_lr : h.lr;
-  const float gs = h.d_gscale ? *h.d_gscale : 1.f;
-  const float ic1 = -1.f / expm1f((float)((double)t * h.log_b1));         // 1 / (1 - b1^t)
-  const float ic2 = rsqrtf(-expm1f((float)((double)t * h.log_b2)));       // 1 / sqrt(1 - b2^t)
+  Consts c;
+  c.b1 = h.b1; c.c1 = h.c1; c.b2 = h.b2; c.c2 = h.c2; c.eps = h.eps;
+  c.lr = h.d_lr ? *h.d_lr : h.lr;
+  c.gs = h.d_gscale ? *h.d_gscale : 1.f;
+  c.ic1 = -1.f / expm1f((float)((double)t * h.log_b1));
+  c.ic2 = rsqrtf(-expm1f((float)((double)t * h.log_b2)));
+  c.t = (uint32_t)t;
+  c.seed = h.seed;
   if (h.d_t && h.advance) {  // the last CTA to have read the count steps it
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -205,55 +483,24 @@ __global__ void __launch_bounds__(256) k_adamw(const __grid_constant__ AdTable<k
     }
   }
   const int lane = threadIdx.x & 31;
-  int li = -1;
+  int li = 0, end = 0;  // the tensor of the last block, and the first block after it
   for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < tb.total_blocks; b += gridDim.x * 8) {
-    li = tensor_of(tb, b, li);
+    if (b >= end) {
+      li = tensor_of(tb, b, li);
+      end = li + 1 < tb.n_tensors ? tb.t[li + 1].block_begin : tb.total_blocks;
+    }
     const AdTensor& T = tb.t[li];
-    const int64_t n = T.n, blk = b - T.block_begin, e0 = blk * kAdBlock + lane * 8;
-    const bool vec = (T.flags & kAdVec) && e0 + 8 <= n;
-    const bool ws = T.flags & kAdWStride, gst = T.flags & kAdGStride;
-    float g[8], w[8], m[8], v[8];
-    load(reinterpret_cast<const GT*>(T.g), e0, n, T.cols, T.g_ld, gst, vec, g);
-    if (kMaster) load(T.master, e0, n, T.cols, 0, false, vec, w);
-    else load(reinterpret_cast<const WT*>(T.w), e0, n, T.cols, T.w_ld, ws, vec, w);
-    if (k8) {
-      const uint32_t sc = *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk);
-      decode8(load_codes(reinterpret_cast<const uint8_t*>(T.m), e0, n, vec), scale_of(sc & 255u), m);
-      decode8(load_codes(reinterpret_cast<const uint8_t*>(T.v), e0, n, vec), scale_of(sc >> 8), v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(v[k], v[k]);  // exact: a code has four significant bits
-    } else {
-      load(reinterpret_cast<const float*>(T.m), e0, n, T.cols, 0, false, vec, m);
-      load(reinterpret_cast<const float*>(T.v), e0, n, T.cols, 0, false, vec, v);
+    const int64_t blk = b - T.block_begin;
+    bool done = false;
+    if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) {
+      if (Kind<kKind>::eight) {
+        done = step_block8<kKind>(T, blk, lane, c, h);
+      } else {
+        step_block32<kKind>(T, blk, lane, c);
+        done = true;
+      }
     }
-    const float wd = T.wd, step = lr * T.lr_scale;
-    float r[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] = __fmul_rn(gs, g[k]);
-      m[k] = __fadd_rn(__fmul_rn(h.b1, m[k]), __fmul_rn(h.c1, g[k]));
-      v[k] = __fadd_rn(__fmul_rn(h.b2, v[k]), __fmul_rn(h.c2, __fmul_rn(g[k], g[k])));
-      r[k] = __fsqrt_rn(v[k]);
-      const float u = (m[k] * ic1) / fmaf(r[k], ic2, h.eps);
-      w[k] = fmaf(-step, fmaf(wd, w[k], u), w[k]);
-    }
-    if (kMaster) store(T.master, e0, n, T.cols, 0, false, vec, w);
-    store(reinterpret_cast<WT*>(T.w), e0, n, T.cols, T.w_ld, ws, vec, w);
-    if (k8) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (!vec && e0 + k >= n) m[k] = r[k] = 0.f;  // entries past a short last block
-      const uint32_t bm = block_exponent(m), br = block_exponent(r);
-      const uint64_t grp = (uint64_t)e0 >> 3;
-      const uint4 rnd =
-          crng::philox4x32_10(make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), (uint32_t)t, 1u), h.seed, T.id);
-      store_codes(reinterpret_cast<uint8_t*>(T.m), e0, n, vec, encode8<true>(m, bm, rnd));
-      store_codes(reinterpret_cast<uint8_t*>(T.v), e0, n, vec, encode8<true>(r, br, rnd));
-      if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
-    } else {
-      store(reinterpret_cast<float*>(T.m), e0, n, T.cols, 0, false, vec, m);
-      store(reinterpret_cast<float*>(T.v), e0, n, T.cols, 0, false, vec, v);
-    }
+    if (!done) step_block_any<kKind>(T, blk, lane, c);
   }
 }
 
@@ -295,9 +542,12 @@ template cudaError_t launch_adamw<kAdMany>(int, const AdTable<kAdMany>&, const A
 __global__ void __launch_bounds__(256) k_grad_sumsq(const __grid_constant__ NormTable tb) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double acc = 0.0;
-  int li = -1;
+  int li = 0, end = 0;
   for (int b = blockIdx.x * 8 + warp; b < tb.total_blocks; b += gridDim.x * 8) {
-    li = tensor_of(tb, b, li);
+    if (b >= end) {
+      li = tensor_of(tb, b, li);
+      end = li + 1 < tb.n_tensors ? tb.t[li + 1].block_begin : tb.total_blocks;
+    }
     const NormTensor& T = tb.t[li];
     const int64_t n = T.n, e0 = (int64_t)(b - T.block_begin) * kAdBlock + lane * 8;
     const bool vec = T.vec && e0 + 8 <= n, st = T.ld != T.cols;
@@ -366,9 +616,12 @@ cudaError_t launch_grad_norm_finish(const NormOut& o, cudaStream_t s) {
 // ---------------------------------------------------------------- conversion
 __global__ void __launch_bounds__(256) k_adamw_convert(const __grid_constant__ ConvTable tb) {
   const int lane = threadIdx.x & 31;
-  int li = -1;
+  int li = 0, end = 0;
   for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < tb.total_blocks; b += gridDim.x * 8) {
-    li = tensor_of(tb, b, li);
+    if (b >= end) {
+      li = tensor_of(tb, b, li);
+      end = li + 1 < tb.n_tensors ? tb.t[li + 1].block_begin : tb.total_blocks;
+    }
     const ConvTensor& T = tb.t[li];
     const int64_t n = T.n, blk = b - T.block_begin, e0 = blk * kAdBlock + lane * 8;
     const bool vec = T.vec && e0 + 8 <= n;
