@@ -1313,12 +1313,13 @@ smuon_status check_tensor(const smuon_mat& a, const char* what, int i, int32_t d
 
 int64_t entries(const smuon_mat& a) { return (int64_t)a.rows * a.cols; }
 int64_t blocks_of(int64_t n) { return (n + kAdBlock - 1) / kAdBlock; }
+int64_t tiles_of(int64_t n) { return (n + kAdTile - 1) / kAdTile; }
 bool has_stride(const smuon_mat& a) { return a.rows > 1 && a.ld != a.cols; }
 
-// whether every eight entries from a multiple of eight on are one aligned vector: 32 bytes of F32, 16 of BF16, 8 codes
-bool vec8(const smuon_mat& a) {
-  const int bytes = 8 * dtype_size(a.dtype);
-  return reinterpret_cast<uintptr_t>(a.data) % bytes == 0 && (!has_stride(a) || (a.cols % 8 == 0 && a.ld % 8 == 0));
+// whether every `k` (8 or 16) entries from a multiple of k on are aligned vectors: at most 32 bytes each, all in one row
+bool vec_of(const smuon_mat& a, int k) {
+  const int bytes = std::min(32, k * dtype_size(a.dtype));
+  return reinterpret_cast<uintptr_t>(a.data) % bytes == 0 && (!has_stride(a) || (a.cols % k == 0 && a.ld % k == 0));
 }
 
 // memory that a call reads or writes: rows of row_bytes, pitch bytes apart
@@ -1457,7 +1458,10 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
     T.n = n; T.cols = W.cols; T.w_ld = W.ld; T.g_ld = G[i].ld;
     T.lr_scale = ls; T.wd = wd; T.id = (uint32_t)i;
     T.flags = (has_stride(W) ? kAdWStride : 0) | (has_stride(G[i]) ? kAdGStride : 0);
-    if (vec8(W) && vec8(G[i]) && vec8(st->m[i]) && vec8(st->v[i]) && (!master || vec8(st->master[i]))) T.flags |= kAdVec;
+    const int lane = eight ? 16 : 8;
+    if (vec_of(W, lane) && vec_of(G[i], lane) && vec_of(st->m[i], lane) && vec_of(st->v[i], lane) &&
+        (!master || vec_of(st->master[i], lane)))
+      T.flags |= kAdVec;
     const int kind = (master ? AD_W_MASTER : W.dtype == SMUON_BF16 ? AD_W_BF16 : AD_W_F32) |
                      (G[i].dtype == SMUON_BF16 ? AD_G_BF16 : 0) | (eight ? AD_8BIT : 0);
     by_kind[kind].push_back(T);
@@ -1475,9 +1479,9 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
     const double per = w_bytes + (kind & AD_G_BF16 ? 2 : 4) + (eight ? 4 : 16);
     for (size_t i = 0; i < ts.size();) {
       size_t j = i;
-      int64_t blocks = 0;
-      while (j < ts.size() && j - i < (size_t)kAdMany && blocks + blocks_of(ts[j].n) < ((int64_t)1 << 30) + 1)
-        blocks += blocks_of(ts[j++].n);
+      int64_t tiles = 0;
+      while (j < ts.size() && j - i < (size_t)kAdMany && tiles + tiles_of(ts[j].n) <= ((int64_t)1 << 30))
+        tiles += tiles_of(ts[j++].n);
       AdExec::Part P;
       P.kind = kind;
       P.few = j - i <= (size_t)kAdFew;
@@ -1486,19 +1490,19 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
       if (P.few) {
         P.small.reset(new AdTable<kAdFew>());
         P.small->n_tensors = (int32_t)(j - i);
-        P.small->total_blocks = (int32_t)blocks;
+        P.small->total_tiles = (int32_t)tiles;
         dst = P.small->t;
       } else {
         P.large.reset(new AdTable<kAdMany>());
         P.large->n_tensors = (int32_t)(j - i);
-        P.large->total_blocks = (int32_t)blocks;
+        P.large->total_tiles = (int32_t)tiles;
         dst = P.large->t;
       }
       int32_t begin = 0;
       for (; i < j; ++i, ++dst) {
         *dst = ts[i];
-        dst->block_begin = begin;
-        begin += (int32_t)blocks_of(ts[i].n);
+        dst->tile_begin = begin;
+        begin += (int32_t)tiles_of(ts[i].n);
         P.bytes += per * (double)ts[i].n + (eight ? 4.0 * (double)blocks_of(ts[i].n) : 0.0);
       }
       ex->parts.push_back(std::move(P));
@@ -1588,7 +1592,7 @@ void norm_tables(const smuon_mat* G, int32_t n, double* ws, std::vector<std::uni
     T.ld = has_stride(G[i]) ? G[i].ld : G[i].cols;
     T.block_begin = (int32_t)blocks;
     T.bf16 = G[i].dtype == SMUON_BF16;
-    T.vec = vec8(G[i]);
+    T.vec = vec_of(G[i], 8);
     blocks += blocks_of(e);
     by += (double)e * dtype_size(G[i].dtype);
   }
@@ -1758,7 +1762,7 @@ smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* strea
       T.m32 = s32->m[i].data; T.v32 = s32->v[i].data; T.m8 = s8->m[i].data; T.v8 = s8->v[i].data;
       T.scales = s8->scales[i];
       T.n = n;
-      T.vec = vec8(s32->m[i]) && vec8(s32->v[i]) && vec8(s8->m[i]) && vec8(s8->v[i]);
+      T.vec = vec_of(s32->m[i], 8) && vec_of(s32->v[i], 8) && vec_of(s8->m[i], 8) && vec_of(s8->v[i], 8);
       ts.push_back(T);
     }
     if ((s = check_overlap(spans)) != SMUON_OK) return s;

@@ -8,7 +8,8 @@
 
 namespace smuon {
 
-constexpr int kAdBlock = 256;  // entries per block: one warp, eight per lane; the 8-bit states' scale group
+constexpr int kAdBlock = 256;  // entries per block, the 8-bit moments' scale group
+constexpr int kAdTile = 512;   // two blocks: what a warp steps at once
 
 // One tensor of a launch. States and master are contiguous; W and G may have a row stride.
 struct AdTensor {
@@ -20,12 +21,12 @@ struct AdTensor {
   uint8_t* scales;        // 8-bit states: two exponent bytes per block (m, root of v)
   int64_t n, w_ld, g_ld;
   int32_t cols;
-  int32_t block_begin;    // first block of this tensor in the launch
+  int32_t tile_begin;     // first tile of this tensor in the launch
   float lr_scale, wd;
   uint32_t id;            // index in the call's lists: key word 1 of its rounding stream
   int32_t flags;          // kAd*
 };
-constexpr int32_t kAdVec = 1;      // every lane's eight entries are one aligned vector in each operand
+constexpr int32_t kAdVec = 1;      // a lane's entries (eight, with 8-bit moments sixteen) are aligned vectors in each operand
 constexpr int32_t kAdWStride = 2;  // W has a row stride
 constexpr int32_t kAdGStride = 4;
 
@@ -48,7 +49,7 @@ struct AdHyper {
 constexpr int kAdFew = 16, kAdMany = 320;
 template <int kCap>
 struct AdTable {
-  int32_t n_tensors, total_blocks;
+  int32_t n_tensors, total_tiles;
   AdTensor t[kCap];
 };
 

@@ -175,13 +175,17 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte, con
   return make_uint2(out[0], out[1]);
 }
 
-// last tensor whose first block is at or before b; li: one known to begin at or before b
+__device__ __forceinline__ int begin_of(const AdTensor& T) { return T.tile_begin; }
+template <class Tensor>
+__device__ __forceinline__ int begin_of(const Tensor& T) { return T.block_begin; }
+
+// last tensor that begins at or before b; li: one known to
 template <class Table>
 __device__ __forceinline__ int tensor_of(const Table& tb, int b, int li) {
   int lo = li, hi = tb.n_tensors - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (tb.t[mid].block_begin <= b) lo = mid; else hi = mid - 1;
+    if (begin_of(tb.t[mid]) <= b) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
@@ -325,45 +329,83 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.x) : "l"(a.x), "l"(b.x), "l"(c.x));
   return d;
 }
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.x) : "l"(a.x), "l"(b.x));
-  return d;
-}
 // a + b as a 1 + b, with a one that the assembler does not know to be one: it contracts mul.rn.f32x2 and add.rn.f32x2
 // into a single rounding (with -fmad=false, too), and the moments need both
 __device__ __forceinline__ F2 add2(F2 a, F2 b, float2 one) { return fma2(a, two(one.x, one.y), b); }
-// eight codes to their values (no scale); two float32 patterns to two codes in the low half
-__device__ __forceinline__ void unpack_codes(const uint2 c, float (&x)[8]) {
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    x[2 * k] = f.x;
-    x[2 * k + 1] = f.y;
-  }
+// two codes (in the low half) to their values without scale; two float32 patterns to two codes in the low half
+__device__ __forceinline__ F2 values_of(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return two(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t codes_of(uint32_t lo, uint32_t hi) {
   uint16_t d;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
   return d;
 }
-// largest magnitude of eight; NaN if one is
+
+// sixteen consecutive entries as loaded, and pairs of them as float32
+template <class E>
+struct Raw16;
+template <>
+struct Raw16<float> {
+  uint32_t lo[8], hi[8];
+  __device__ __forceinline__ void from(const char* p) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[k];
+      uint32_t* u = k < 2 ? lo + 4 * k : hi + 4 * k - 8;
+      u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+    }
+  }
+  __device__ __forceinline__ void store(float* p) const { st256(p, lo); st256(p + 8, hi); }
+  __device__ __forceinline__ F2 pair(int k) const {
+    const uint32_t* u = k < 8 ? lo + k : hi + k - 8;
+    return two(__uint_as_float(u[0]), __uint_as_float(u[1]));
+  }
+  __device__ __forceinline__ void put(int k, float a, float b) {
+    uint32_t* u = k < 8 ? lo + k : hi + k - 8;
+    u[0] = __float_as_uint(a);
+    u[1] = __float_as_uint(b);
+  }
+};
+template <>
+struct Raw16<__nv_bfloat16> {
+  uint32_t u[8];
+  __device__ __forceinline__ void from(const char* p) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[k];
+      u[4 * k] = x.x; u[4 * k + 1] = x.y; u[4 * k + 2] = x.z; u[4 * k + 3] = x.w;
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { st256(p, u); }
+  __device__ __forceinline__ F2 pair(int k) const {
+    return two(add_bf16((uint16_t)u[k >> 1]), add_bf16((uint16_t)(u[k >> 1] >> 16)));
+  }
+  __device__ __forceinline__ void put(int k, float a, float b) { u[k >> 1] = pack2(a, b); }
+};
+
+// largest of three magnitudes; NaN if one is
 __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   float d;
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float max_abs8(const float (&x)[8]) {
-  return max_abs3(max_abs3(max_abs3(x[0], x[1], x[2]), x[3], x[4]), max_abs3(x[5], x[6], x[7]), 0.f);
+// largest magnitude of the sixteen lanes' sixteen values each that this lane belongs to
+__device__ __forceinline__ float half_warp_max(const float (&x)[16], bool upper) {
+  float t = fabsf(x[0]);
+#pragma unroll
+  for (int k = 1; k < 15; k += 2) t = max_abs3(t, x[k], x[k + 1]);
+  const uint32_t u = __float_as_uint(max_abs3(t, x[15], x[15]));  // NaN above infinity above all, as integers too
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, upper ? 0u : u), hi = __reduce_max_sync(0xffffffffu, upper ? u : 0u);
+  return __uint_as_float(upper ? hi : lo);
 }
 
 // random words of a group of eight entries: Philox4x32-10 with the seed's key schedule from the parameters
-__device__ __forceinline__ uint4 group_words(int64_t e0, const Consts& c, const uint32_t (&k0)[10], uint32_t k1) {
-  const uint64_t grp = (uint64_t)e0 >> 3;
-  uint4 x = make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), c.t, 1u);
+__device__ __forceinline__ uint4 group_words(uint64_t grp, uint32_t t, const uint32_t (&k0)[10], uint32_t k1) {
+  uint4 x = make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), t, 1u);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     if (r) k1 += 0xBB67AE85u;
@@ -373,67 +415,123 @@ __device__ __forceinline__ uint4 group_words(int64_t e0, const Consts& c, const 
   return x;
 }
 
-// A whole block with vector operands, 8-bit moments: the same values as step_block_any with fewer instructions, which
-// are what bounds it.
+// A warp's stage of shared memory: the operands of one tile as they lie in global memory.
+template <int kKind>
+struct Stage {
+  using K = Kind<kKind>;
+  using ST = typename std::conditional<K::master, float, typename K::W>::type;  // the weights that are stepped
+  static constexpr int w = 0, g = w + kAdTile * (int)sizeof(ST), m = g + kAdTile * (int)sizeof(typename K::G),
+                       v = m + kAdTile, bytes = v + kAdTile;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// tile of a contiguous operand, 16 bytes a lane at a time
+template <class E>
+__device__ __forceinline__ void copy_operand(uint32_t dst, const void* base, int tile, uint32_t lane16) {
+  const char* src = reinterpret_cast<const char*>(base) + lane16 + (uint64_t)(uint32_t)tile * (kAdTile * sizeof(E));
+#pragma unroll
+  for (int k = 0; k < kAdTile * (int)sizeof(E); k += 512) copy16(dst + lane16 + k, src + k);
+}
+// the first `entries` entries of a tile of an operand that may have a row stride
+template <class E>
+__device__ __noinline__ void copy_rows(uint32_t dst, const void* base, int64_t e0, int entries, int lane, int32_t cols, int64_t ld) {
+  constexpr int per = 16 / sizeof(E);
+#pragma unroll 1
+  for (int k = lane * per; k < entries; k += 32 * per)
+    copy16(dst + k * (int)sizeof(E), reinterpret_cast<const E*>(base) + strided(e0 + k, cols, ld));
+}
+
+// starts the copies of a tile's whole blocks; returns the lane's block's exponent bytes
+template <int kKind>
+__device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int lane, uint32_t stage) {
+  using L = Stage<kKind>;
+  using K = Kind<kKind>;
+  using ST = typename L::ST;
+  using GT = typename K::G;
+  const void* const w = K::master ? T.master : T.w;
+  if ((int64_t)(tile + 1) * kAdTile <= T.n && (T.flags & (kAdVec | kAdWStride | kAdGStride)) == kAdVec) {
+    const uint32_t lane16 = lane * 16;
+    copy_operand<GT>(stage + L::g, T.g, tile, lane16);
+    copy_operand<uint8_t>(stage + L::m, T.m, tile, lane16);
+    copy_operand<uint8_t>(stage + L::v, T.v, tile, lane16);
+    copy_operand<ST>(stage + L::w, w, tile, lane16);
+    return reinterpret_cast<const uint16_t*>(T.scales)[2 * (int64_t)tile + (lane >> 4)];
+  }
+  const int64_t e0 = (int64_t)tile * kAdTile, whole = T.n / kAdBlock - 2 * (int64_t)tile;
+  if (!(T.flags & kAdVec) || whole < 1) return 0;
+  const int entries = whole > 1 ? kAdTile : kAdBlock;
+  const bool ws = !K::master && (T.flags & kAdWStride), gst = T.flags & kAdGStride;  // without a stride: one row
+  copy_rows<GT>(stage + L::g, reinterpret_cast<const GT*>(T.g) + (gst ? 0 : e0), gst ? e0 : 0, entries, lane, gst ? T.cols : kAdTile, T.g_ld);
+  copy_rows<ST>(stage + L::w, reinterpret_cast<const ST*>(w) + (ws ? 0 : e0), ws ? e0 : 0, entries, lane, ws ? T.cols : kAdTile, T.w_ld);
+  copy_rows<uint8_t>(stage + L::m, reinterpret_cast<const uint8_t*>(T.m) + e0, 0, entries, lane, kAdTile, 0);
+  copy_rows<uint8_t>(stage + L::v, reinterpret_cast<const uint8_t*>(T.v) + e0, 0, entries, lane, kAdTile, 0);
+  return reinterpret_cast<const uint16_t*>(T.scales)[2 * (int64_t)tile + (whole > 1 && lane >= 16)];
+}
+
+// The whole blocks of a tile with vector operands, 8-bit moments, a block to each half of the warp (sixteen entries a
+// lane: what a block costs beside its entries is then paid once for two): the same values as step_block_any with fewer
+// instructions, which are what bounds it.
 //  - b1 m = (b1 2^k) code and b2 v = (b2 2^2k) code^2: a power of two commutes with the rounding, so the factor is
 //    formed once a block (while it is a normal number).
 //  - r' only goes into W' and into its code, which depends on r' through the carry out of its 20 low bits. An
 //    approximate root, made smaller by 2^-21 of itself, is below r' by less than 16 units in the last place and gives
-//    the same code unless those bits are within 16 of a carry: the warp then (one block in 250) takes exact roots. The
+//    the same code unless those bits are within 16 of a carry: the warp then (one tile in 125) takes exact roots. The
 //    block's exponent comes from the exact root of the largest v' (rounding is monotonic).
 // false where a value leaves the range in which this holds (nothing is written then).
 template <int kKind>
-__device__ __forceinline__ bool step_block8(const AdTensor& T, int64_t blk, int lane, const Consts& c,
-                                            const AdHyper& h) {
+__device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane, const Consts& c, const AdHyper& h,
+                                           const char* stage, uint32_t sc) {
   using K = Kind<kKind>;
+  using L = Stage<kKind>;
   using WT = typename K::W;
-  using GT = typename K::G;
-  const int64_t e0 = blk * kAdBlock + lane * 8;
-  const int64_t wo = T.flags & kAdWStride ? strided(e0, T.cols, T.w_ld) : e0;
-  const int64_t go = T.flags & kAdGStride ? strided(e0, T.cols, T.g_ld) : e0;
-  float m[8], v[8], w[8];
+  const bool upper = lane >= 16;
+  const bool on = (2 * (int64_t)tile + upper + 1) * kAdBlock <= T.n;  // else the upper half repeats the lower one's block and stores nothing
+  const int at = (on ? lane : lane - 16) * 16;
+  const int64_t e0 = (int64_t)tile * kAdTile + at;
+  float m[16], v[16];
   {
-    float g[8];
-    const uint32_t sc = *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk);
-    const uint2 cm = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(T.m) + e0);
-    const uint2 cr = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(T.v) + e0);
-    ld8(reinterpret_cast<const GT*>(T.g) + go, g);
-    if (K::master) ld8(T.master + e0, w);
-    else ld8(reinterpret_cast<const WT*>(T.w) + wo, w);
+    Raw16<typename K::G> g;
+    const uint4 cm = *reinterpret_cast<const uint4*>(stage + L::m + at), cr = *reinterpret_cast<const uint4*>(stage + L::v + at);
+    g.from(stage + L::g + at * (int)sizeof(typename K::G));
     const float sm = scale_of(sc & 255u), sr = scale_of(sc >> 8);
     const float b1s = c.b1 * sm, b2s = c.b2 * (sr * sr);
     // exact factors: zero, or normal with room on both sides
-    if (!((sm == 0.f || (b1s >= 0x1p-100f && b1s <= 0x1p100f)) && (sr == 0.f || (b2s >= 0x1p-100f && b2s <= 0x1p100f))))
-      return false;
-    unpack_codes(cm, m);
-    unpack_codes(cr, v);
+    const bool ok = (sm == 0.f || (b1s >= 0x1p-100f && b1s <= 0x1p100f)) && (sr == 0.f || (b2s >= 0x1p-100f && b2s <= 0x1p100f));
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const uint32_t wm[4] = {cm.x, cm.y, cm.z, cm.w}, wr[4] = {cr.x, cr.y, cr.z, cr.w};
     const F2 gs = both(c.gs), b1 = both(b1s), c1 = two(h.c1_2.x, h.c1_2.y), b2 = both(b2s), c2 = two(h.c2_2.x, h.c2_2.y);
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const F2 g2 = mul2(gs, two(g[k], g[k + 1])), v2 = two(v[k], v[k + 1]);
-      split(add2(mul2(b1, two(m[k], m[k + 1])), mul2(c1, g2), h.one2), m[k], m[k + 1]);
-      split(add2(mul2(b2, mul2(v2, v2)), mul2(c2, mul2(g2, g2)), h.one2), v[k], v[k + 1]);
+    for (int k = 0; k < 16; k += 2) {
+      const F2 g2 = mul2(gs, g.pair(k)), m2 = values_of(wm[k >> 2] >> (8 * (k & 2))), r2 = values_of(wr[k >> 2] >> (8 * (k & 2)));
+      split(add2(mul2(b1, m2), mul2(c1, g2), h.one2), m[k], m[k + 1]);
+      split(add2(mul2(b2, mul2(r2, r2)), mul2(c2, mul2(g2, g2)), h.one2), v[k], v[k + 1]);
     }
   }
-  const float tm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m))));
-  const float tv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v))));
+  const float tm = half_warp_max(m, upper), tv = half_warp_max(v, upper);
   // finite, and so large (or zero) that the smallest v' which the root does not flush to zero is far below the codes
-  if (!(tm <= 0x1p120f && tv <= 0x1p120f && (tv == 0.f || tv >= 0x1p-80f))) return false;
+  if (!__all_sync(0xffffffffu, tm <= 0x1p120f && tv <= 0x1p120f && (tv == 0.f || tv >= 0x1p-80f))) return false;
   const uint32_t fm = __float_as_uint(tm) >> 23, fr = __float_as_uint(__fsqrt_rn(tv)) >> 23;
   const uint32_t bm = fm > 7u ? fm - 7u : 0u, br = fr > 7u ? fr - 7u : 0u;
   const F2 um = both(bm ? __uint_as_float((254u - bm) << 23) : 0.f);
   const F2 ur = both(br ? __uint_as_float(((254u - br) << 23) - 8u) : 0.f);  // (1 - 2^-21) 2^j
-  const uint4 rnd = group_words(e0, c, h.k0, T.id);
-  const uint32_t rw[4] = {rnd.x, rnd.y, rnd.z, rnd.w};
+  const uint64_t grp = (uint64_t)e0 >> 3;
+  const uint4 ra = group_words(grp, c.t, h.k0, T.id), rb = group_words(grp + 1, c.t, h.k0, T.id);
+  const uint32_t rw[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
   const float lr = c.lr * T.lr_scale;
   const F2 step = both(-lr * c.ic1), decay = both(-lr * T.wd), ic2 = both(c.ic2), eps = two(h.eps2.x, h.eps2.y);
-  uint32_t om[2], orr[2], near = 0xffffffffu;
+  Raw16<typename L::ST> w;
+  w.from(stage + L::w + at * (int)sizeof(typename L::ST));
+  uint32_t om[4], orr[4], near = 0xffffffffu;
 #pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    const F2 m2 = two(m[k], m[k + 1]), r2 = two(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), w2 = two(w[k], w[k + 1]);
+  for (int k = 0; k < 16; k += 2) {
+    const F2 m2 = two(m[k], m[k + 1]), r2 = two(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), w2 = w.pair(k);
     float d0, d1, a0, a1, b0, b1;
     split(fma2(r2, ic2, eps), d0, d1);
-    split(fma2(step, mul2(m2, two(rcp_approx(d0), rcp_approx(d1))), fma2(decay, w2, w2)), w[k], w[k + 1]);
+    split(fma2(step, mul2(m2, two(rcp_approx(d0), rcp_approx(d1))), fma2(decay, w2, w2)), a0, a1);
+    w.put(k, a0, a1);
     split(mul2(m2, um), a0, a1);
     split(mul2(r2, ur), b0, b1);
     const uint32_t h0 = __byte_perm(rw[k >> 1], 0, 0x4410), h1 = __byte_perm(rw[k >> 1], 0, 0x4432);
@@ -444,25 +542,40 @@ __device__ __forceinline__ bool step_block8(const AdTensor& T, int64_t blk, int 
     om[k >> 2] = k & 2 ? __byte_perm(om[k >> 2], a, 0x5410) : a;
     orr[k >> 2] = k & 2 ? __byte_perm(orr[k >> 2], b, 0x5410) : b;
   }
-  uint2 codes_r = make_uint2(orr[0], orr[1]);
   if (__any_sync(0xffffffffu, near == 0u)) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __fsqrt_rn(v[k]);
-    codes_r = encode8<true>(v, br, rnd);
+    for (int k = 0; k < 16; k += 8) {
+      float r[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = __fsqrt_rn(v[k + j]);
+      const uint2 x = encode8<true>(r, br, k ? rb : ra);
+      orr[k >> 2] = x.x;
+      orr[(k >> 2) + 1] = x.y;
+    }
   }
-  if (K::master) st8(T.master + e0, w);
-  st8(reinterpret_cast<WT*>(T.w) + wo, w);
-  *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(T.m) + e0) = make_uint2(om[0], om[1]);
-  *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(T.v) + e0) = codes_r;
-  if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
+  if (!on) return true;
+  WT* const pw = reinterpret_cast<WT*>(T.w) + (T.flags & kAdWStride ? strided(e0, T.cols, T.w_ld) : e0);
+  if constexpr (K::master) {
+    w.store(T.master + e0);
+    Raw16<WT> b;
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      float x, y;
+      split(w.pair(k), x, y);
+      b.put(k, x, y);
+    }
+    b.store(pw);
+  } else {
+    w.store(pw);
+  }
+  *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(T.m) + e0) = make_uint4(om[0], om[1], om[2], om[3]);
+  *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(T.v) + e0) = make_uint4(orr[0], orr[1], orr[2], orr[3]);
+  if ((lane & 15) == 0) reinterpret_cast<uint16_t*>(T.scales)[2 * (int64_t)tile + upper] = (uint16_t)(bm | br << 8);
   return true;
 }
 
-}  // namespace
-
-template <int kKind, int kCap>
-__global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdTable<kCap> tb, const __grid_constant__ AdHyper h) {
-  if (h.skip && *h.skip) return;
+// the call's numbers; the last CTA to have read the step count steps it
+__device__ __forceinline__ Consts consts_of(const AdHyper& h) {
   const int64_t t = h.d_t ? *h.d_t + 1 : h.t;
   Consts c;
   c.b1 = h.b1; c.c1 = h.c1; c.b2 = h.b2; c.c2 = h.c2; c.eps = h.eps;
@@ -472,7 +585,7 @@ __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdTabl
   c.ic2 = rsqrtf(-expm1f((float)((double)t * h.log_b2)));
   c.t = (uint32_t)t;
   c.seed = h.seed;
-  if (h.d_t && h.advance) {  // the last CTA to have read the count steps it
+  if (h.d_t && h.advance) {
     __syncthreads();
     if (threadIdx.x == 0) {
       __threadfence();
@@ -482,34 +595,92 @@ __global__ void __launch_bounds__(256, 4) k_adamw(const __grid_constant__ AdTabl
       }
     }
   }
-  const int lane = threadIdx.x & 31;
-  int li = 0, end = 0;  // the tensor of the last block, and the first block after it
-  for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < tb.total_blocks; b += gridDim.x * 8) {
+  return c;
+}
+
+// a warp's walk over the tiles of a launch
+template <int kCap>
+struct Walk {
+  int b, li, end;  // tile, its tensor, the first tile after that tensor
+  __device__ __forceinline__ bool seek(const AdTable<kCap>& tb) {
+    if (b >= tb.total_tiles) return false;
     if (b >= end) {
       li = tensor_of(tb, b, li);
-      end = li + 1 < tb.n_tensors ? tb.t[li + 1].block_begin : tb.total_blocks;
+      end = li + 1 < tb.n_tensors ? tb.t[li + 1].tile_begin : tb.total_tiles;
     }
-    const AdTensor& T = tb.t[li];
-    const int64_t blk = b - T.block_begin;
-    bool done = false;
-    if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) {
-      if (Kind<kKind>::eight) {
-        done = step_block8<kKind>(T, blk, lane, c, h);
-      } else {
-        step_block32<kKind>(T, blk, lane, c);
-        done = true;
-      }
+    return true;
+  }
+};
+
+}  // namespace
+
+template <int kKind, int kCap>
+__global__ void __launch_bounds__(256, 4) k_adamw32(const __grid_constant__ AdTable<kCap> tb, const __grid_constant__ AdHyper h) {
+  if (h.skip && *h.skip) return;
+  const Consts c = consts_of(h);
+  const int lane = threadIdx.x & 31;
+  Walk<kCap> at{(int)(blockIdx.x * 8 + (threadIdx.x >> 5)), 0, 0};
+  for (; at.seek(tb); at.b += gridDim.x * 8) {
+    const AdTensor& T = tb.t[at.li];
+    const int64_t tile = at.b - T.tile_begin, blocks = (T.n + kAdBlock - 1) / kAdBlock - 2 * tile;
+    for (int k = 0; k < 2 && k < blocks; ++k) {
+      const int64_t blk = 2 * tile + k;
+      if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) step_block32<kKind>(T, blk, lane, c);
+      else step_block_any<kKind>(T, blk, lane, c);
     }
-    if (!done) step_block_any<kKind>(T, blk, lane, c);
+  }
+}
+
+// Each warp has two stages of its own: the next tile's operands are on their way into one (cp.async) while the other is
+// stepped. Deeper rings (up to four stages) and five or six CTAs an SM measured the same or slower: the pipes of the
+// arithmetic, not the loads, are what is left.
+constexpr int kAd8Warps = 4, kAd8Ctas = 4;
+template <int kKind, int kCap>
+__global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __grid_constant__ AdTable<kCap> tb,
+                                                                     const __grid_constant__ AdHyper h) {
+  using L = Stage<kKind>;
+  extern __shared__ __align__(16) char smem[];
+  if (h.skip && *h.skip) return;
+  const Consts c = consts_of(h);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, stride = gridDim.x * kAd8Warps;
+  char* const ring = smem + warp * 2 * L::bytes;
+  const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
+  Walk<kCap> next{(int)(blockIdx.x * kAd8Warps + warp), 0, 0};
+  bool more = next.seek(tb);
+  uint32_t sc_next = 0;
+  if (more) sc_next = fetch_tile8<kKind>(tb.t[next.li], next.b - tb.t[next.li].tile_begin, lane, ring_addr);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  for (int turn = 0; more; turn ^= 1) {
+    const AdTensor& T = tb.t[next.li];
+    const int tile = next.b - T.tile_begin;
+    const int64_t whole = T.n / kAdBlock - 2 * (int64_t)tile;
+    const uint32_t sc = sc_next;
+    next.b += stride;
+    more = next.seek(tb);
+    __syncwarp();  // every lane has read the stage that is filled now
+    if (more)
+      sc_next = fetch_tile8<kKind>(tb.t[next.li], next.b - tb.t[next.li].tile_begin, lane, ring_addr + (turn ^ 1) * L::bytes);
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    int k = 0;  // the tile's first block that is not done
+    if ((T.flags & kAdVec) && whole > 0 && step_tile8<kKind>(T, tile, lane, c, h, ring + turn * L::bytes, sc))
+      k = whole > 1 ? 2 : 1;
+    for (; k < 2 && (2 * (int64_t)tile + k) * kAdBlock < T.n; ++k) step_block_any<kKind>(T, 2 * (int64_t)tile + k, lane, c);
   }
 }
 
 namespace {
 template <int kKind, int kCap>
 cudaError_t launch_kind(const AdTable<kCap>& tb, const AdHyper& h, int sms, cudaStream_t s) {
-  const int want = (tb.total_blocks + 7) / 8;
-  const int grid = want < 1 ? 1 : (want < sms * 8 ? want : sms * 8);
-  k_adamw<kKind, kCap><<<grid, 256, 0, s>>>(tb, h);
+  if constexpr (Kind<kKind>::eight) {
+    const int want = (tb.total_tiles + kAd8Warps - 1) / kAd8Warps;
+    const int grid = want < 1 ? 1 : (want < sms * kAd8Ctas ? want : sms * kAd8Ctas);
+    k_adamw8<kKind, kCap><<<grid, 32 * kAd8Warps, kAd8Warps * 2 * Stage<kKind>::bytes, s>>>(tb, h);
+  } else {
+    const int want = (tb.total_tiles + 7) / 8;
+    const int grid = want < 1 ? 1 : (want < sms * 8 ? want : sms * 8);
+    k_adamw32<kKind, kCap><<<grid, 256, 0, s>>>(tb, h);
+  }
   return cudaGetLastError();
 }
 }  // namespace
