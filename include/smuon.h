@@ -476,8 +476,8 @@ smuon_status lionmuon_step(lionmuon_state* st, int32_t P, float beta1, float bet
  * Tensors. W and G may have a row stride (ld > cols); master, m and v are the
  * optimizer's own and must be contiguous (ld == cols). rows and cols may be
  * any non-negative int32 (a tensor with no entries is skipped, and its data
- * may be NULL). No limit on n_tensors; up to 320 tensors of one combination of
- * types go into one launch.
+ * may be NULL). No limit on n_tensors; without a plan up to 320 tensors of one
+ * combination of types go into one launch.
  *
  * 8-bit moments (m and v of type SMUON_E4M3). m holds the first moment, v the
  * square root of the second (a code spans 2^16 of a block's values, enough
@@ -530,10 +530,14 @@ smuon_status adamw_step(adamw_state* st, const smuon_mat* G, double lr, double b
 
 /* The step prepared once: the addresses in st and G, beta1, beta2, eps and the device pointers are kept (also
  * weight_decay and lr_scale as they are now); adamw_execute takes t and the learning rate anew (st->t is incremented;
- * st->d_t and st->seed are those of creation). Executing is capturable; a captured step counts on only with d_t. */
+ * st->d_t and st->seed are those of creation). The table of more than 16 tensors of one combination of types is uploaded
+ * into ws on `stream` (ws: adamw_plan_workspace_bytes(), 256-byte aligned, kept as long as the plan; executions follow
+ * that upload in stream order), so any number of tensors is one launch per combination. Executing is capturable; a
+ * captured step counts on only with d_t. */
+smuon_status adamw_plan_workspace_bytes(const adamw_state* st, size_t* bytes);
 smuon_status adamw_plan_create(const adamw_state* st, const smuon_mat* G, double beta1, double beta2, double eps,
                                const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if,
-                               smuon_plan* out);
+                               void* ws, size_t ws_bytes, void* stream, smuon_plan* out);
 smuon_status adamw_execute(smuon_plan plan, adamw_state* st, double lr, void* stream);
 
 /* dst's moments <- src's moments, from F32 to SMUON_E4M3 or back (the other direction of types, or two states of one
@@ -546,15 +550,16 @@ smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* strea
  * that clips the gradients to max_norm (> 0; infinity: never clips). Where the norm is not a finite float32, d_out[1] =
  * 0, *d_skip = 1 (else 0; nullable) and SMUON_DEV_NONFINITE_NORM is OR-ed into *d_status (nullable). Squares are summed
  * in float32 over eight entries and in float64 above, in a fixed order; every gradient whose norm float32 holds gets it,
- * however small or large its entries. G as in adamw_step (F32 and BF16 may be mixed; n_tensors >= 1). ws: scratch of
+ * however small or large its entries. G as in adamw_step (F32 and BF16 may be mixed; n_tensors >= 1). ws:
  * smuon_grad_norm_workspace_bytes(), 256-byte aligned, not shared with a call that may run concurrently. The plan form
- * keeps ws, the addresses and max_norm. */
+ * uploads its table into ws on `stream` once, keeps ws, the addresses and max_norm, and is one launch; executions of one
+ * plan follow that upload, and one another, in stream order. */
 smuon_status smuon_grad_norm_workspace_bytes(const smuon_mat* G, int32_t n_tensors, size_t* bytes);
 smuon_status smuon_grad_norm(const smuon_mat* G, int32_t n_tensors, double max_norm, float* d_out, int32_t* d_skip,
                              void* ws, size_t ws_bytes, int32_t* d_status, void* stream);
 smuon_status smuon_grad_norm_plan_create(const smuon_mat* G, int32_t n_tensors, double max_norm, float* d_out,
                                          int32_t* d_skip, void* ws, size_t ws_bytes, int32_t* d_status,
-                                         smuon_plan* out);
+                                         void* stream, smuon_plan* out);
 smuon_status smuon_grad_norm_execute(smuon_plan plan, void* stream);
 
 #ifdef __cplusplus

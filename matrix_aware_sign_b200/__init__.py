@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_double, c_float, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 import torch
@@ -126,15 +127,16 @@ def lib() -> ctypes.CDLL:
                                         c_void_p, c_void_p]),
             "adamw_step": (c_int32, [POINTER(AdamWState), M, c_double, c_double, c_double, c_double, c_void_p,
                                      c_void_p, c_void_p, c_void_p]),
+            "adamw_plan_workspace_bytes": (c_int32, [POINTER(AdamWState), POINTER(c_size_t)]),
             "adamw_plan_create": (c_int32, [POINTER(AdamWState), M, c_double, c_double, c_double, c_void_p, c_void_p,
-                                            c_void_p, POINTER(c_void_p)]),
+                                            c_void_p, c_void_p, c_size_t, c_void_p, POINTER(c_void_p)]),
             "adamw_execute": (c_int32, [c_void_p, POINTER(AdamWState), c_double, c_void_p]),
             "adamw_convert": (c_int32, [POINTER(AdamWState), POINTER(AdamWState), c_void_p]),
             "smuon_grad_norm_workspace_bytes": (c_int32, [M, c_int32, POINTER(c_size_t)]),
             "smuon_grad_norm": (c_int32, [M, c_int32, c_double, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
                                           c_void_p]),
             "smuon_grad_norm_plan_create": (c_int32, [M, c_int32, c_double, c_void_p, c_void_p, c_void_p, c_size_t,
-                                                      c_void_p, POINTER(c_void_p)]),
+                                                      c_void_p, c_void_p, POINTER(c_void_p)]),
             "smuon_grad_norm_execute": (c_int32, [c_void_p, c_void_p]),
         }
         for name, (res, args) in sigs.items():
@@ -200,8 +202,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -450,21 +452,31 @@ def smuon_harness_gaussian(G, workers: int, stream_desc: GradStream, step: int, 
 _DT_TENSOR = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
 
 
-def tensor(t) -> SmuonMat:
-    """Describes a tensor of any shape for the AdamW calls: contiguous, or 2-D with unit column stride."""
-    if t.dtype not in _DT_TENSOR:
+def _describe(t):
+    """(data, rows, cols, ld, dtype) of a tensor of any shape: contiguous, or 2-D with unit column stride."""
+    dt = _DT_TENSOR.get(t.dtype)
+    if dt is None:
         raise ValueError(f"dtype {t.dtype} is not supported")
-    n, ptr, dt = t.numel(), t.data_ptr(), _DT_TENSOR[t.dtype]
+    n = t.numel()
     if n == 0:
-        return SmuonMat(None, 0, 0, 0, dt)
+        return 0, 0, 0, 0, dt
     if t.is_contiguous():
         cols = t.shape[-1] if t.dim() else 1
         if max(cols, n // cols) >= 1 << 31:
             raise ValueError("at most 2^31 - 1 rows and columns: view the tensor in another shape")
-        return SmuonMat(ptr, n // cols, cols, cols, dt)
+        return t.data_ptr(), n // cols, cols, cols, dt
     if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError("tensors must be contiguous, or 2-D with unit column stride and rows that do not overlap")
-    return SmuonMat(ptr, t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1], dt)
+    return t.data_ptr(), t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1], dt
+
+
+def tensor(t) -> SmuonMat:
+    """Describes a tensor for the AdamW calls: contiguous of any shape, or 2-D with unit column stride."""
+    ptr, rows, cols, ld, dt = _describe(t)
+    return SmuonMat(ptr or None, rows, cols, ld, dt)
+
+
+_MAT = struct.Struct("@QiiqiI")  # SmuonMat
 
 
 def _tensors(ts, shapes=None, name="G"):
@@ -473,9 +485,13 @@ def _tensors(ts, shapes=None, name="G"):
         if len(ts) != len(shapes):
             raise ValueError(f"{len(ts)} tensors in {name}, {len(shapes)} weights")
         for i, (t, s) in enumerate(zip(ts, shapes)):
-            if t is not None and tuple(t.shape) != s:
-                raise ValueError(f"{name}[{i}] has shape {tuple(t.shape)}, its weight {s}")
-    return (SmuonMat * len(ts))(*[SmuonMat() if t is None else tensor(t) for t in ts])
+            if t is not None and t.shape != s:
+                raise ValueError(f"{name}[{i}] has shape {tuple(t.shape)}, its weight {tuple(s)}")
+    arr = (SmuonMat * len(ts))()
+    for i, t in enumerate(ts):  # packed in place: a SmuonMat object for each takes twice as long
+        if t is not None:
+            _MAT.pack_into(arr, i * _MAT.size, *_describe(t), 0)
+    return arr
 
 
 def _one_device(*groups) -> torch.device:
@@ -517,7 +533,7 @@ class AdamW:
                  t=0, device_step=False):
         self.W = list(W)
         n = len(self.W)
-        shapes = [tuple(w.shape) for w in self.W]
+        shapes = [w.shape for w in self.W]
         if (m is None) != (v is None) or (m is None and scales is not None):
             raise ValueError("give m and v together (with scales for 8-bit moments), or none of them")
         if m is None:
@@ -586,7 +602,36 @@ def adamw_step(opt: AdamW, G, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=N
                                 _ptr(d_lr), _ptr(grad_scale), _ptr(skip_if), _stream(stream)))
 
 
-class AdamWPlan:
+class _Prepared:
+    """A plan whose table was uploaded on the stream that was current then. Runs on that stream follow the upload by
+    themselves; the first run on another stream waits for it."""
+    handle = None
+
+    def _uploading(self, device):
+        """To be entered around the creation: its device, and no capture (the upload would be the graph's)."""
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("prepare the plan before the capture: its table is uploaded once")
+        self._index = device.index
+        return torch.cuda.device(device)
+
+    def _uploaded(self):
+        self._made = _stream(None)
+        self._ready, self._seen = torch.cuda.Event(), {self._made}
+        self._ready.record()
+
+    def _follow(self, s):
+        if not torch.cuda.is_current_stream_capturing():  # a capture begins after all that was uploaded before it
+            torch.cuda.ExternalStream(s).wait_event(self._ready)
+            self._seen.add(s)
+
+    def __del__(self):
+        h = self.handle
+        if h and _lib is not None:
+            _lib.smuon_plan_destroy(h)
+            self.handle = None
+
+
+class AdamWPlan(_Prepared):
     """adamw_step prepared once, for gradients that keep their addresses; run()
     enqueues only the kernels. `lr` may be a device tensor here, or a number in run()."""
 
@@ -595,25 +640,26 @@ class AdamWPlan:
             raise ValueError("lr must be a device tensor here: give a number to run()")
         mats, d_lr = _adamw_args(opt, G, lr, grad_scale, skip_if)
         self.opt, self.tensors = opt, (list(G), d_lr, grad_scale, skip_if)  # keep the buffers alive
-        h = c_void_p()
-        with torch.cuda.device(opt.device):
+        h, n = c_void_p(), c_size_t(0)
+        with self._uploading(opt.device):
+            _check(lib().adamw_plan_workspace_bytes(ctypes.byref(opt.state), ctypes.byref(n)))
+            self.ws = workspace(n.value, opt.device)
             _check(lib().adamw_plan_create(ctypes.byref(opt.state), mats, beta1, beta2, eps, _ptr(d_lr),
-                                           _ptr(grad_scale), _ptr(skip_if), ctypes.byref(h)))
-        self.handle, self._state, self._index = h, ctypes.byref(opt.state), opt.device.index
+                                           _ptr(grad_scale), _ptr(skip_if), self.ws.data_ptr(), self.ws.numel(),
+                                           _stream(None), ctypes.byref(h)))
+            self._uploaded()
+        self.handle, self._state, self._device_lr = h, ctypes.byref(opt.state), d_lr is not None
 
     def run(self, lr=None, stream=None):
-        if (lr is None) != (self.tensors[1] is not None):
+        if (lr is None) != self._device_lr:
             raise ValueError("give lr once: as a device tensor to the plan, or as a number here")
         if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.run(lr, stream)
-        _check(lib().adamw_execute(self.handle, self._state, 0.0 if lr is None else lr, _stream(stream)))
-
-    def __del__(self):
-        h = getattr(self, "handle", None)
-        if h and _lib is not None:
-            _lib.smuon_plan_destroy(h)
-            self.handle = None
+        s = _stream(stream)
+        if s not in self._seen:
+            self._follow(s)
+        _check(lib().adamw_execute(self.handle, self._state, 0.0 if lr is None else lr, s))
 
 
 def adamw_convert(src: AdamW, dst: AdamW, stream=None):
@@ -631,11 +677,11 @@ def smuon_grad_norm_workspace_bytes(G) -> int:
     return out.value
 
 
-class GradNorm:
-    """Global 2-norm of many gradients, prepared once; run() enqueues only the
-    kernels. On the device afterwards: norm, coef = min(1, max_norm / (norm +
-    1e-6)) (one-element float32 tensors) and skip (int32: 1 where the norm is
-    not finite; coef is then 0)."""
+class GradNorm(_Prepared):
+    """Global 2-norm of many gradients that keep their addresses, prepared once;
+    run() enqueues one kernel. On the device afterwards: norm, coef = min(1,
+    max_norm / (norm + 1e-6)) (float32 scalars) and skip (int32: 1 where the
+    norm is not finite; coef is then 0)."""
 
     def __init__(self, G, max_norm: float, status=None):
         G = list(G)
@@ -643,26 +689,25 @@ class GradNorm:
         self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
         self.norm, self.coef = self.out[0], self.out[1]
         self.skip = torch.zeros((), dtype=torch.int32, device=self.device)
-        self.ws = workspace(smuon_grad_norm_workspace_bytes(G), self.device)
         self.tensors = (G, _scalar(status, torch.int32, "status"))  # keep the buffers alive
-        h = c_void_p()
-        with torch.cuda.device(self.device):
-            _check(lib().smuon_grad_norm_plan_create(_tensors(G), len(G), max_norm, self.out.data_ptr(),
+        h, mats, n = c_void_p(), _tensors(G), c_size_t(0)
+        with self._uploading(self.device):
+            _check(lib().smuon_grad_norm_workspace_bytes(mats, len(G), ctypes.byref(n)))
+            self.ws = workspace(n.value, self.device)
+            _check(lib().smuon_grad_norm_plan_create(mats, len(G), max_norm, self.out.data_ptr(),
                                                      self.skip.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
-                                                     _ptr(status), ctypes.byref(h)))
+                                                     _ptr(status), _stream(None), ctypes.byref(h)))
+            self._uploaded()
         self.handle = h
 
     def run(self, stream=None):
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
                 return self.run(stream)
-        _check(lib().smuon_grad_norm_execute(self.handle, _stream(stream)))
-
-    def __del__(self):
-        h = getattr(self, "handle", None)
-        if h and _lib is not None:
-            _lib.smuon_plan_destroy(h)
-            self.handle = None
+        s = _stream(stream)
+        if s not in self._seen:
+            self._follow(s)
+        _check(lib().smuon_grad_norm_execute(self.handle, s))
 
 
 def smuon_grad_norm(G, max_norm: float, out, skip=None, ws=None, status=None, stream=None):

@@ -660,6 +660,24 @@ smuon_status build_plan(const NsRequest& rq, char* base, Builder* B) {
   return SMUON_OK;
 }
 
+// copies `size` bytes (a multiple of 16) to dst on the stream, as kernel parameters
+smuon_status upload_bytes(const unsigned char* bytes, size_t size, char* dst, cudaStream_t s) {
+  static UploadChunk chunk;  // large parameter block; filled then launched by value
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  for (size_t off = 0; off < size; off += kUploadBytes) {
+    const size_t n = std::min(size - off, (size_t)kUploadBytes);
+    chunk.dst = dst + off;
+    chunk.bytes = (int32_t)n;
+    memcpy(chunk.data, bytes + off, n);
+    const int blocks = (int)std::min<size_t>(8, (n / 16 + 255) / 256);
+    Launch L("k_plan_upload", SMUON_WORK_BYTES, 2.0 * n, s);
+    k_plan_upload<<<std::max(blocks, 1), 256, 0, s>>>(chunk);
+    CUDA_TRY(cudaGetLastError());
+  }
+  return SMUON_OK;
+}
+
 smuon_status upload_plan(Builder& B, cudaStream_t s) {
   std::vector<unsigned char> bytes(B.L.plan_bytes, 0);
   Plan p;
@@ -681,20 +699,7 @@ smuon_status upload_plan(Builder& B, cudaStream_t s) {
   }
   memcpy(bytes.data() + B.L.off_sched_begin, B.sched_begin.data(), sizeof(int32_t) * B.sched_begin.size());
   if (B.L.n_tmaps > 0) memcpy(bytes.data() + B.L.off_tmaps, B.maps.data(), sizeof(CUtensorMap) * B.L.n_tmaps);
-  static UploadChunk chunk;  // large parameter block; filled then launched by value
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lk(mu);
-  for (size_t off = 0; off < bytes.size(); off += kUploadBytes) {
-    const size_t n = std::min(bytes.size() - off, (size_t)kUploadBytes);
-    chunk.dst = B.base + off;
-    chunk.bytes = (int32_t)n;
-    memcpy(chunk.data, bytes.data() + off, n);
-    const int blocks = (int)std::min<size_t>(8, (n / 16 + 255) / 256);
-    Launch L("k_plan_upload", SMUON_WORK_BYTES, 2.0 * n, s);
-    k_plan_upload<<<std::max(blocks, 1), 256, 0, s>>>(chunk);
-    CUDA_TRY(cudaGetLastError());
-  }
-  return SMUON_OK;
+  return upload_bytes(bytes.data(), bytes.size(), B.base, s);
 }
 
 // algorithmic flops of one stage over the whole batch: 2 * Mo * No * K per matrix
@@ -1347,7 +1352,21 @@ bool meet(const Span& a, const Span& b) {
 }
 
 smuon_status check_overlap(std::vector<Span>& v) {
-  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  // by address, from the runs that are in order already (a list of views of one buffer is one run)
+  std::vector<size_t> runs{0};
+  auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  for (size_t j = 1; j < v.size(); ++j)
+    if (before(v[j], v[j - 1])) runs.push_back(j);
+  runs.push_back(v.size());
+  while (runs.size() > 2) {
+    std::vector<size_t> merged{0};
+    for (size_t k = 0; k + 2 < runs.size(); k += 2) {
+      std::inplace_merge(v.begin() + runs[k], v.begin() + runs[k + 1], v.begin() + runs[k + 2], before);
+      merged.push_back(runs[k + 2]);
+    }
+    if (merged.back() != v.size()) merged.push_back(v.size());
+    runs.swap(merged);
+  }
   // spans still open at v[j]: read ones are compared with written ones only
   std::vector<size_t> open;
   for (size_t j = 0; j < v.size(); ++j) {
@@ -1365,12 +1384,12 @@ smuon_status check_overlap(std::vector<Span>& v) {
 }
 
 struct AdExec {
-  struct Part {  // one launch
-    int kind;
-    bool few;
-    double bytes;
+  struct Part {  // one launch; its table in one of the three places
+    int kind = 0;
+    double bytes = 0;
     std::unique_ptr<AdTable<kAdFew>> small;
     std::unique_ptr<AdTable<kAdMany>> large;
+    AdDevTable dev{};
   };
   std::vector<Part> parts;
   AdHyper h{};
@@ -1413,18 +1432,35 @@ smuon_status check_state(const adamw_state* st, bool* eight) {
   return SMUON_OK;
 }
 
-void add_moments(std::vector<Span>& v, const adamw_state* st, int i, bool eight, bool written) {
-  add_span(v, st->m[i], written, "m", i);
-  add_span(v, st->v[i], written, "v", i);
-  if (eight) {
+void add_spans(std::vector<Span>& v, const smuon_mat* a, int n, bool written, const char* what) {
+  for (int i = 0; i < n; ++i) add_span(v, a[i], written, what, i);
+}
+void add_moments(std::vector<Span>& v, const adamw_state* st, bool eight, bool written) {
+  add_spans(v, st->m, st->n_tensors, written, "m");
+  add_spans(v, st->v, st->n_tensors, written, "v");
+  for (int i = 0; eight && i < st->n_tensors; ++i) {
     const int64_t n = entries(st->W[i]);
     const uintptr_t p = reinterpret_cast<uintptr_t>(st->scales[i]);
     if (n) v.push_back(Span{p, p + 2 * (uintptr_t)blocks_of(n), 0, 0, false, written, "scales", i});
   }
 }
 
+// launches of a table: at most `most` tensors and 2^30 tiles each
+template <class F>
+void split_tensors(const std::vector<AdTensor>& ts, size_t most, F&& part) {
+  for (size_t i = 0; i < ts.size();) {
+    size_t j = i;
+    int64_t tiles = 0;
+    while (j < ts.size() && j - i < most && tiles + tiles_of(ts[j].n) <= ((int64_t)1 << 30)) tiles += tiles_of(ts[j++].n);
+    part(i, j, (int32_t)tiles);
+    i = j;
+  }
+}
+size_t adamw_ws_bytes(int64_t n_tensors) { return (size_t)round_up(std::max<int64_t>(n_tensors * (int64_t)sizeof(AdTensor), 256), 256); }
+
 smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double beta1, double beta2, double eps,
-                           const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if, AdExec* ex) {
+                           const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if, bool plan, void* ws,
+                           size_t ws_bytes, cudaStream_t stream, AdExec* ex) {
   bool eight = false;
   smuon_status s = check_state(st, &eight);
   if (s != SMUON_OK) return s;
@@ -1447,10 +1483,6 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
     const int64_t n = entries(W);
     if (!n) continue;
     const bool master = st->master && st->master[i].data;
-    add_span(spans, W, true, "W", i);
-    add_span(spans, G[i], false, "G", i);
-    if (master) add_span(spans, st->master[i], true, "master", i);
-    add_moments(spans, st, i, eight, true);
     AdTensor T{};
     T.w = W.data; T.g = G[i].data; T.m = st->m[i].data; T.v = st->v[i].data;
     T.master = master ? reinterpret_cast<float*>(st->master[i].data) : nullptr;
@@ -1466,36 +1498,44 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
                      (G[i].dtype == SMUON_BF16 ? AD_G_BF16 : 0) | (eight ? AD_8BIT : 0);
     by_kind[kind].push_back(T);
   }
+  spans.reserve(7 * (size_t)st->n_tensors + 1);
+  add_spans(spans, st->W, st->n_tensors, true, "W");
+  add_spans(spans, G, st->n_tensors, false, "G");
+  for (int i = 0; st->master && i < st->n_tensors; ++i)
+    if (st->master[i].data) add_span(spans, st->master[i], true, "master", i);
+  add_moments(spans, st, eight, true);
   if (st->d_t) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(st->d_t);
     spans.push_back(Span{p, p + 16, 0, 0, false, true, "d_t", 0});
   }
   if ((s = check_overlap(spans)) != SMUON_OK) return s;
+  if (plan && (s = check_ws(ws, ws_bytes, adamw_ws_bytes(st->n_tensors))) != SMUON_OK) return s;
   if ((s = device_info(&ex->di)) != SMUON_OK) return s;
   ex->parts.clear();
+  std::vector<AdTensor> table;  // what goes into ws
   for (int kind = 0; kind < AD_KINDS; ++kind) {
     const std::vector<AdTensor>& ts = by_kind[kind];
     const double w_bytes = (kind & 3) == AD_W_F32 ? 8 : (kind & 3) == AD_W_BF16 ? 4 : 10;
     const double per = w_bytes + (kind & AD_G_BF16 ? 2 : 4) + (eight ? 4 : 16);
-    for (size_t i = 0; i < ts.size();) {
-      size_t j = i;
-      int64_t tiles = 0;
-      while (j < ts.size() && j - i < (size_t)kAdMany && tiles + tiles_of(ts[j].n) <= ((int64_t)1 << 30))
-        tiles += tiles_of(ts[j++].n);
+    const bool in_ws = plan && ts.size() > (size_t)kAdFew;
+    split_tensors(ts, in_ws ? ts.size() : kAdMany, [&](size_t i, size_t j, int32_t tiles) {
       AdExec::Part P;
       P.kind = kind;
-      P.few = j - i <= (size_t)kAdFew;
-      P.bytes = 0;
       AdTensor* dst;
-      if (P.few) {
+      const size_t first = table.size();
+      if (in_ws) {
+        table.resize(first + (j - i));
+        dst = table.data() + first;
+        P.dev = AdDevTable{(int32_t)(j - i), tiles, reinterpret_cast<const AdTensor*>(ws) + first};
+      } else if (j - i <= (size_t)kAdFew) {
         P.small.reset(new AdTable<kAdFew>());
         P.small->n_tensors = (int32_t)(j - i);
-        P.small->total_tiles = (int32_t)tiles;
+        P.small->total_tiles = tiles;
         dst = P.small->t;
       } else {
         P.large.reset(new AdTable<kAdMany>());
         P.large->n_tensors = (int32_t)(j - i);
-        P.large->total_tiles = (int32_t)tiles;
+        P.large->total_tiles = tiles;
         dst = P.large->t;
       }
       int32_t begin = 0;
@@ -1506,16 +1546,19 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
         P.bytes += per * (double)ts[i].n + (eight ? 4.0 * (double)blocks_of(ts[i].n) : 0.0);
       }
       ex->parts.push_back(std::move(P));
-    }
+    });
   }
   if (ex->parts.empty() && st->d_t) {  // no entries at all: the count still advances
     AdExec::Part P;
     P.kind = AD_W_F32;
-    P.few = true;
     P.bytes = 16;
     P.small.reset(new AdTable<kAdFew>());
     ex->parts.push_back(std::move(P));
   }
+  static_assert(sizeof(AdTensor) % 16 == 0, "uploads move 16 bytes at a time");
+  if (!table.empty() && (s = upload_bytes(reinterpret_cast<const unsigned char*>(table.data()), table.size() * sizeof(AdTensor),
+                                          reinterpret_cast<char*>(ws), stream)) != SMUON_OK)
+    return s;
   AdHyper& h = ex->h;
   h.skip = d_skip_if; h.d_lr = d_lr; h.d_gscale = d_grad_scale; h.d_t = st->d_t;
   h.log_b1 = std::log(beta1); h.log_b2 = std::log(beta2);
@@ -1541,18 +1584,17 @@ smuon_status run_adamw(const AdExec& ex, adamw_state* st, double lr, cudaStream_
     const AdExec::Part& P = ex.parts[i];
     h.advance = i + 1 == ex.parts.size();
     Launch L(adamw_name(P.kind), SMUON_WORK_BYTES, P.bytes, s);
-    CUDA_TRY(P.few ? launch_adamw<kAdFew>(P.kind, *P.small, h, ex.di.sms, s)
-                   : launch_adamw<kAdMany>(P.kind, *P.large, h, ex.di.sms, s));
+    CUDA_TRY(P.small   ? launch_adamw(P.kind, *P.small, h, ex.di.sms, s)
+             : P.large ? launch_adamw(P.kind, *P.large, h, ex.di.sms, s)
+                       : launch_adamw(P.kind, P.dev, h, ex.di.sms, s));
   }
   st->t += 1;
   return SMUON_OK;
 }
 
 struct NormExec {
-  std::vector<std::unique_ptr<NormTable>> tables;
-  std::vector<double> bytes;
-  NormOut o{};
-  DevInfo di;
+  NormArgs a{};
+  double bytes = 0;
 };
 
 smuon_status check_norm_tensors(const smuon_mat* G, int32_t n) {
@@ -1565,70 +1607,56 @@ smuon_status check_norm_tensors(const smuon_mat* G, int32_t n) {
   return SMUON_OK;
 }
 
-// launches of a norm over G, with their partial sums' place in ws (host only: ws NULL to size it)
-void norm_tables(const smuon_mat* G, int32_t n, double* ws, std::vector<std::unique_ptr<NormTable>>* out,
-                 std::vector<double>* bytes, int32_t* n_partials) {
-  *n_partials = 0;
-  std::unique_ptr<NormTable> tb;
-  int64_t blocks = 0;
-  double by = 0;
-  auto flush = [&] {
-    if (!tb) return;
-    tb->total_blocks = (int32_t)blocks;
-    tb->partials = ws ? ws + *n_partials : nullptr;
-    *n_partials += norm_grid(tb->total_blocks);
-    out->push_back(std::move(tb));
-    bytes->push_back(by);
-    blocks = 0;
-    by = 0;
-  };
-  for (int i = 0; i < n; ++i) {
-    const int64_t e = entries(G[i]);
-    if (!e) continue;
-    if (tb && (tb->n_tensors == kNormMany || blocks + blocks_of(e) > ((int64_t)1 << 30))) flush();
-    if (!tb) tb.reset(new NormTable());
-    NormTensor& T = tb->t[tb->n_tensors++];
-    T.g = G[i].data; T.n = e; T.cols = G[i].cols;
-    T.ld = has_stride(G[i]) ? G[i].ld : G[i].cols;
-    T.block_begin = (int32_t)blocks;
-    T.bf16 = G[i].dtype == SMUON_BF16;
-    T.vec = vec_of(G[i], 8);
-    blocks += blocks_of(e);
-    by += (double)e * dtype_size(G[i].dtype);
-  }
-  flush();
-}
-
-size_t norm_ws_bytes(int32_t n_partials) { return (size_t)round_up(std::max<int64_t>(8 * (int64_t)n_partials, 256), 256); }
+// ws of a norm: the arrival count, the table, one partial sum per CTA
+constexpr size_t kNormHead = 256;
+size_t norm_table_bytes(int32_t n) { return (size_t)round_up((int64_t)n * (int64_t)sizeof(NormTensor), 256); }
+size_t norm_ws_bytes(int32_t n) { return kNormHead + norm_table_bytes(n) + (size_t)round_up(8 * kNormMaxGrid, 256); }
 
 smuon_status prepare_norm(const smuon_mat* G, int32_t n, double max_norm, float* d_out, int32_t* d_skip, void* ws,
-                          size_t ws_bytes, int32_t* d_status, NormExec* ex) {
+                          size_t ws_bytes, int32_t* d_status, cudaStream_t stream, NormExec* ex) {
   smuon_status s = check_norm_tensors(G, n);
   if (s != SMUON_OK) return s;
   if (!d_out) return fail(SMUON_ERR_INVALID_ARG, "d_out is NULL");
   if ((reinterpret_cast<uintptr_t>(d_out) | reinterpret_cast<uintptr_t>(d_skip) | reinterpret_cast<uintptr_t>(d_status)) % 4)
     return fail(SMUON_ERR_INVALID_ARG, "d_out, d_skip and d_status must be 4-byte aligned");
   if (!(max_norm > 0)) return fail(SMUON_ERR_INVALID_ARG, "max_norm=%g must be > 0", max_norm);
-  int32_t parts = 0;
-  norm_tables(G, n, reinterpret_cast<double*>(ws), &ex->tables, &ex->bytes, &parts);
-  if ((s = check_ws(ws, ws_bytes, norm_ws_bytes(parts))) != SMUON_OK) return s;
-  if ((s = device_info(&ex->di)) != SMUON_OK) return s;
-  ex->o.partials = reinterpret_cast<const double*>(ws);
-  ex->o.n_partials = parts;
-  ex->o.max_norm = max_norm;
-  ex->o.out = d_out;
-  ex->o.skip = d_skip;
-  ex->o.status = d_status;
+  if ((s = check_ws(ws, ws_bytes, norm_ws_bytes(n))) != SMUON_OK) return s;
+  std::vector<unsigned char> bytes(kNormHead + norm_table_bytes(n), 0);
+  NormTensor* const t = reinterpret_cast<NormTensor*>(bytes.data() + kNormHead);
+  int32_t used = 0;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t e = entries(G[i]);
+    if (!e) continue;
+    NormTensor& T = t[used++];
+    T.g = G[i].data; T.n = e; T.cols = G[i].cols;
+    T.ld = has_stride(G[i]) ? G[i].ld : G[i].cols;
+    T.tile_begin = (int32_t)tiles;
+    T.bf16 = G[i].dtype == SMUON_BF16;
+    T.vec = vec_of(G[i], 8);
+    tiles += (e + kNormTile - 1) / kNormTile;
+    if (tiles > ((int64_t)1 << 30)) return fail(SMUON_ERR_UNSUPPORTED, "more than 2^40 entries in all");
+    ex->bytes += (double)e * dtype_size(G[i].dtype);
+  }
+  DevInfo di;
+  if ((s = device_info(&di)) != SMUON_OK) return s;
+  char* const base = reinterpret_cast<char*>(ws);
+  if ((s = upload_bytes(bytes.data(), bytes.size(), base, stream)) != SMUON_OK) return s;
+  ex->a.t = reinterpret_cast<const NormTensor*>(base + kNormHead);
+  ex->a.n_tensors = used;
+  ex->a.total_tiles = (int32_t)tiles;
+  ex->a.partials = reinterpret_cast<double*>(base + bytes.size());
+  ex->a.arrived = reinterpret_cast<uint32_t*>(base);
+  ex->a.max_norm = max_norm;
+  ex->a.out = d_out;
+  ex->a.skip = d_skip;
+  ex->a.status = d_status;
   return SMUON_OK;
 }
 
 smuon_status run_norm(const NormExec& ex, cudaStream_t s) {
-  for (size_t i = 0; i < ex.tables.size(); ++i) {
-    Launch L("k_grad_sumsq", SMUON_WORK_BYTES, ex.bytes[i], s);
-    CUDA_TRY(launch_grad_norm(*ex.tables[i], s));
-  }
-  Launch L("k_grad_norm_finish", SMUON_WORK_BYTES, 8.0 * ex.o.n_partials + 8, s);
-  CUDA_TRY(launch_grad_norm_finish(ex.o, s));
+  Launch L("k_grad_norm", SMUON_WORK_BYTES, ex.bytes, s);
+  CUDA_TRY(launch_grad_norm(ex.a, s));
   return SMUON_OK;
 }
 
@@ -1711,21 +1739,29 @@ smuon_status adamw_step(adamw_state* st, const smuon_mat* G, double lr, double b
                         const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if, void* stream) {
   return guarded([&]() -> smuon_status {
     AdExec ex;
-    smuon_status s = prepare_adamw(st, G, beta1, beta2, eps, d_lr, d_grad_scale, d_skip_if, &ex);
+    smuon_status s = prepare_adamw(st, G, beta1, beta2, eps, d_lr, d_grad_scale, d_skip_if, false, nullptr, 0, nullptr, &ex);
     if (s != SMUON_OK) return s;
     return run_adamw(ex, st, lr, reinterpret_cast<cudaStream_t>(stream));
   });
 }
 
+smuon_status adamw_plan_workspace_bytes(const adamw_state* st, size_t* bytes) {
+  if (!st || !bytes) return fail(SMUON_ERR_INVALID_ARG, "NULL argument");
+  if (st->n_tensors < 1) return fail(SMUON_ERR_INVALID_ARG, "n_tensors < 1");
+  *bytes = adamw_ws_bytes(st->n_tensors);
+  return SMUON_OK;
+}
+
 smuon_status adamw_plan_create(const adamw_state* st, const smuon_mat* G, double beta1, double beta2, double eps,
-                               const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if,
-                               smuon_plan* out) {
+                               const float* d_lr, const float* d_grad_scale, const int32_t* d_skip_if, void* ws,
+                               size_t ws_bytes, void* stream, smuon_plan* out) {
   if (!out) return fail(SMUON_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
   return guarded([&]() -> smuon_status {
     std::unique_ptr<smuon_plan_s> p(new smuon_plan_s());
     p->kind = 2;
-    smuon_status s = prepare_adamw(st, G, beta1, beta2, eps, d_lr, d_grad_scale, d_skip_if, &p->ad);
+    smuon_status s = prepare_adamw(st, G, beta1, beta2, eps, d_lr, d_grad_scale, d_skip_if, true, ws, ws_bytes,
+                                   reinterpret_cast<cudaStream_t>(stream), &p->ad);
     if (s != SMUON_OK) return s;
     *out = p.release();
     return SMUON_OK;
@@ -1756,8 +1792,6 @@ smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* strea
       const int64_t n = entries(src->W[i]);
       if (entries(dst->W[i]) != n) return fail(SMUON_ERR_SHAPE, "tensor %d has %lld and %lld entries", i, (long long)n, (long long)entries(dst->W[i]));
       if (!n) continue;
-      add_moments(spans, src, i, from8, false);
-      add_moments(spans, dst, i, to8, true);
       ConvTensor T{};
       T.m32 = s32->m[i].data; T.v32 = s32->v[i].data; T.m8 = s8->m[i].data; T.v8 = s8->v[i].data;
       T.scales = s8->scales[i];
@@ -1765,6 +1799,9 @@ smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* strea
       T.vec = vec_of(s32->m[i], 8) && vec_of(s32->v[i], 8) && vec_of(s8->m[i], 8) && vec_of(s8->v[i], 8);
       ts.push_back(T);
     }
+    spans.reserve(6 * (size_t)src->n_tensors);
+    add_moments(spans, src, from8, false);
+    add_moments(spans, dst, to8, true);
     if ((s = check_overlap(spans)) != SMUON_OK) return s;
     DevInfo di;
     if ((s = device_info(&di)) != SMUON_OK) return s;
@@ -1773,18 +1810,18 @@ smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* strea
     for (size_t i = 0; i < ts.size();) {
       tb->n_tensors = 0;
       tb->to8 = to8;
-      int64_t blocks = 0;
+      int64_t tiles = 0;
       double bytes = 0;
-      while (i < ts.size() && tb->n_tensors < kAdMany && blocks + blocks_of(ts[i].n) < ((int64_t)1 << 30) + 1) {
+      while (i < ts.size() && tb->n_tensors < kAdMany && tiles + tiles_of(ts[i].n) <= ((int64_t)1 << 30)) {
         tb->t[tb->n_tensors] = ts[i];
-        tb->t[tb->n_tensors++].block_begin = (int32_t)blocks;
-        blocks += blocks_of(ts[i].n);
+        tb->t[tb->n_tensors++].tile_begin = (int32_t)tiles;
+        tiles += tiles_of(ts[i].n);
         bytes += 10.0 * (double)ts[i].n + 2.0 * (double)blocks_of(ts[i].n);
         ++i;
       }
-      tb->total_blocks = (int32_t)blocks;
+      tb->total_tiles = (int32_t)tiles;
       Launch L("k_adamw_convert", SMUON_WORK_BYTES, bytes, strm);
-      CUDA_TRY(launch_adamw_convert(*tb, di.sms, strm));
+      CUDA_TRY(launch_adamw_convert(*tb, strm));
     }
     if (src->d_t && src->d_t != dst->d_t)
       CUDA_TRY(cudaMemcpyAsync(dst->d_t, src->d_t, sizeof(int64_t), cudaMemcpyDeviceToDevice, strm));
@@ -1798,11 +1835,7 @@ smuon_status smuon_grad_norm_workspace_bytes(const smuon_mat* G, int32_t n_tenso
   return guarded([&]() -> smuon_status {
     smuon_status s = check_norm_tensors(G, n_tensors);
     if (s != SMUON_OK) return s;
-    std::vector<std::unique_ptr<NormTable>> tables;
-    std::vector<double> by;
-    int32_t parts = 0;
-    norm_tables(G, n_tensors, nullptr, &tables, &by, &parts);
-    *bytes = norm_ws_bytes(parts);
+    *bytes = norm_ws_bytes(n_tensors);
     return SMUON_OK;
   });
 }
@@ -1811,7 +1844,8 @@ smuon_status smuon_grad_norm(const smuon_mat* G, int32_t n_tensors, double max_n
                              void* ws, size_t ws_bytes, int32_t* d_status, void* stream) {
   return guarded([&]() -> smuon_status {
     NormExec ex;
-    smuon_status s = prepare_norm(G, n_tensors, max_norm, d_out, d_skip, ws, ws_bytes, d_status, &ex);
+    smuon_status s = prepare_norm(G, n_tensors, max_norm, d_out, d_skip, ws, ws_bytes, d_status,
+                                  reinterpret_cast<cudaStream_t>(stream), &ex);
     if (s != SMUON_OK) return s;
     return run_norm(ex, reinterpret_cast<cudaStream_t>(stream));
   });
@@ -1819,13 +1853,14 @@ smuon_status smuon_grad_norm(const smuon_mat* G, int32_t n_tensors, double max_n
 
 smuon_status smuon_grad_norm_plan_create(const smuon_mat* G, int32_t n_tensors, double max_norm, float* d_out,
                                          int32_t* d_skip, void* ws, size_t ws_bytes, int32_t* d_status,
-                                         smuon_plan* out) {
+                                         void* stream, smuon_plan* out) {
   if (!out) return fail(SMUON_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
   return guarded([&]() -> smuon_status {
     std::unique_ptr<smuon_plan_s> p(new smuon_plan_s());
     p->kind = 3;
-    smuon_status s = prepare_norm(G, n_tensors, max_norm, d_out, d_skip, ws, ws_bytes, d_status, &p->norm);
+    smuon_status s = prepare_norm(G, n_tensors, max_norm, d_out, d_skip, ws, ws_bytes, d_status,
+                                  reinterpret_cast<cudaStream_t>(stream), &p->norm);
     if (s != SMUON_OK) return s;
     *out = p.release();
     return SMUON_OK;

@@ -45,58 +45,58 @@ struct AdHyper {
   int32_t advance;        // last launch of the call: the last CTA to read d_t[0] adds one to it
 };
 
-// Tables travel as kernel parameters (32,764 bytes at most). The small one is for calls of few tensors.
+// Tables travel as kernel parameters (32,764 bytes at most) or, with a plan, lie in its workspace. Launching with the
+// large parameter block costs the host 4 us more and the GPU 2 us more than with the small one or a table in memory.
 constexpr int kAdFew = 16, kAdMany = 320;
 template <int kCap>
 struct AdTable {
   int32_t n_tensors, total_tiles;
   AdTensor t[kCap];
 };
+struct AdDevTable {
+  int32_t n_tensors, total_tiles;
+  const AdTensor* t;
+};
 
 enum AdKind { AD_W_F32 = 0, AD_W_BF16 = 1, AD_W_MASTER = 2, AD_G_BF16 = 4, AD_8BIT = 8, AD_KINDS = 16 };
 
-template <int kCap>
-cudaError_t launch_adamw(int kind, const AdTable<kCap>& tb, const AdHyper& h, int sms, cudaStream_t s);
+template <class Table>
+cudaError_t launch_adamw(int kind, const Table& tb, const AdHyper& h, int sms, cudaStream_t s);
 
-// gradient norm: per-CTA sums of squares, then one CTA for the norm, the clip factor and the flags
+// gradient norm: per-CTA sums of squares; the last CTA to finish takes the norm, the clip factor and the flags
+constexpr int kNormTile = 1024;  // entries that a warp squares at once
 struct NormTensor {
   const void* g;
   int64_t n, ld;
   int32_t cols;
-  int32_t block_begin;
+  int32_t tile_begin;
   int32_t bf16, vec;
 };
-constexpr int kNormMany = 512;
-struct NormTable {
-  int32_t n_tensors, total_blocks;
-  double* partials;
-  NormTensor t[kNormMany];
-};
-constexpr int kNormMaxGrid = 1184;
-struct NormOut {
-  const double* partials;
-  int32_t n_partials;
+constexpr int kNormMaxGrid = 592;  // four CTAs an SM (64 registers a thread)
+struct NormArgs {
+  const NormTensor* t;
+  int32_t n_tensors, total_tiles;
+  double* partials;   // one per CTA
+  uint32_t* arrived;  // zero before a launch, and after it
   double max_norm;
-  float* out;        // {norm, factor}
-  int32_t* skip;     // nullable: 1 where the norm is not finite, else 0
-  int32_t* status;   // nullable
+  float* out;         // {norm, factor}
+  int32_t* skip;      // nullable: 1 where the norm is not finite, else 0
+  int32_t* status;    // nullable
 };
-int norm_grid(int total_blocks);
-cudaError_t launch_grad_norm(const NormTable& tb, cudaStream_t s);
-cudaError_t launch_grad_norm_finish(const NormOut& o, cudaStream_t s);
+cudaError_t launch_grad_norm(const NormArgs& a, cudaStream_t s);
 
-// moments from float32 to 8 bits (to8) or back; the 32-bit side may be BF16 on the way back
+// moments from float32 to 8 bits (to8) or back
 struct ConvTensor {
   void *m32, *v32, *m8, *v8;
   uint8_t* scales;
   int64_t n;
-  int32_t block_begin;
+  int32_t tile_begin;
   int32_t vec;
 };
 struct ConvTable {
-  int32_t n_tensors, total_blocks, to8, pad;
+  int32_t n_tensors, total_tiles, to8, pad;
   ConvTensor t[kAdMany];
 };
-cudaError_t launch_adamw_convert(const ConvTable& tb, int sms, cudaStream_t s);
+cudaError_t launch_adamw_convert(const ConvTable& tb, cudaStream_t s);
 
 }  // namespace smuon

@@ -1,8 +1,7 @@
 // k_adamw.cu -- the AdamW step for the parameters beside the Muon matrices.
 //
-//  * k_adamw              one step over many tensors, moments in float32 or in 8 bits
-//  * k_grad_sumsq         sums of squares of many gradients
-//  * k_grad_norm_finish   their norm, the clip factor made from it, the skip flag
+//  * k_adamw32, k_adamw8  one step over many tensors, moments in float32 or in 8 bits
+//  * k_grad_norm          norm of many gradients, the clip factor made from it, the skip flag
 //  * k_adamw_convert      moments from float32 to 8 bits and back
 //
 // The step is Loshchilov and Hutter's ("Decoupled Weight Decay Regularization"):
@@ -11,6 +10,8 @@
 // All arithmetic is float32. m', v' and r' are formed with every operation
 // rounded on its own (no fused multiply-add), so that any IEEE evaluation of
 // the same steps gives the same bits; the 8-bit codes depend on them.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -78,26 +79,24 @@ __device__ __forceinline__ int64_t strided(int64_t e, int32_t cols, int64_t ld) 
   return r * ld + (e - r * cols);
 }
 
+// eight entries from entry e0 on, which lies at element `at` (all eight in one row, where there are eight)
 template <class T>
-__device__ __forceinline__ void load(const T* p, int64_t e0, int64_t n, int32_t cols, int64_t ld, bool stride, bool vec,
-                                     float (&x)[8]) {
+__device__ __forceinline__ void load(const T* p, int64_t e0, int64_t n, int64_t at, bool vec, float (&x)[8]) {
   if (vec) {
-    ld8(p + (stride ? strided(e0, cols, ld) : e0), x);
+    ld8(p + at, x);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      x[k] = e0 + k < n ? to_f32(p[stride ? strided(e0 + k, cols, ld) : e0 + k]) : 0.f;
+    for (int k = 0; k < 8; ++k) x[k] = e0 + k < n ? to_f32(p[at + k]) : 0.f;
   }
 }
 template <class T>
-__device__ __forceinline__ void store(T* p, int64_t e0, int64_t n, int32_t cols, int64_t ld, bool stride, bool vec,
-                                      const float (&x)[8]) {
+__device__ __forceinline__ void store(T* p, int64_t e0, int64_t n, int64_t at, bool vec, const float (&x)[8]) {
   if (vec) {
-    st8(p + (stride ? strided(e0, cols, ld) : e0), x);
+    st8(p + at, x);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (e0 + k < n) put(p + (stride ? strided(e0 + k, cols, ld) : e0 + k), x[k]);
+      if (e0 + k < n) put(p + at + k, x[k]);
   }
 }
 
@@ -175,19 +174,60 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte, con
   return make_uint2(out[0], out[1]);
 }
 
-__device__ __forceinline__ int begin_of(const AdTensor& T) { return T.tile_begin; }
-template <class Tensor>
-__device__ __forceinline__ int begin_of(const Tensor& T) { return T.block_begin; }
-
-// last tensor that begins at or before b; li: one known to
+// last tensor that begins at or before tile b; li: one known to. Binary in a table of kernel parameters
 template <class Table>
 __device__ __forceinline__ int tensor_of(const Table& tb, int b, int li) {
   int lo = li, hi = tb.n_tensors - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (begin_of(tb.t[mid]) <= b) lo = mid; else hi = mid - 1;
+    if (tb.t[mid].tile_begin <= b) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+// in a table in memory: the warp looks at 32 places at once, so a thousand tensors take two loads
+template <class Tensor>
+__device__ __forceinline__ int tensor_of_warp(const Tensor* t, int n, int b, int li) {
+  const int lane = threadIdx.x & 31;
+  for (int len = n - li; len > 1;) {
+    const int step = (len + 31) >> 5, at = li + lane * step;
+    const bool ok = lane * step < len && t[at].tile_begin <= b;
+    const int k = __popc(__ballot_sync(0xffffffffu, ok)) - 1;
+    li += k * step;
+    len = min(step, len - k * step);
+  }
+  return li;
+}
+__device__ __forceinline__ int tensor_of(const AdDevTable& tb, int b, int li) { return tensor_of_warp(tb.t, tb.n_tensors, b, li); }
+
+// A warp's walk over the tiles of a launch.
+template <class Table>
+struct Walk {
+  int b, stop;          // tile, and where the walk stops
+  int li = 0, end = 0;  // the tile's tensor, and the first tile after that tensor
+  int which = 1;        // of the warp's two places in shared memory for tensors of a table in memory, taken in turn
+  __device__ __forceinline__ Walk(int first, int after) : b(first), stop(after) {}
+  __device__ __forceinline__ bool seek(const Table& tb, AdTensor* slots) {
+    if (b >= stop) return false;
+    if (b >= end) {
+      li = tensor_of(tb, b, li);
+      end = li + 1 < tb.n_tensors ? tb.t[li + 1].tile_begin : tb.total_tiles;
+      if constexpr (std::is_same<Table, AdDevTable>::value) {
+        which ^= 1;
+        const int lane = threadIdx.x & 31;
+        __syncwarp();  // every lane is done with the tensor that lay there
+        if (lane < (int)(sizeof(AdTensor) / 4))
+          reinterpret_cast<uint32_t*>(slots + which)[lane] = reinterpret_cast<const uint32_t*>(tb.t + li)[lane];
+        __syncwarp();
+      }
+    }
+    return true;
+  }
+};
+// tensor `li` of a table: in the kernel parameters, or the copy in shared memory
+template <class Table>
+__device__ __forceinline__ const AdTensor& tensor_at(const Table& tb, int li, const AdTensor* slots, int which) {
+  if constexpr (std::is_same<Table, AdDevTable>::value) return slots[which];
+  else return tb.t[li];
 }
 
 // ---------------------------------------------------------------- the step
@@ -222,9 +262,8 @@ __device__ __forceinline__ float sqrt_approx(float v) {
   return r;
 }
 
-// Any block: short ones, operands off their vector addresses, row strides that are no multiple of eight, 8-bit blocks
-// whose scales leave the range of the fast form or whose values are not finite. Entry by entry; with float32 moments
-// the lanes' entries lie side by side, so the accesses coalesce.
+// A block of any alignment or stride, entry by entry; with 8-bit moments also one whose scales leave the range of the fast
+// form or whose values are not finite. With float32 moments the lanes' entries lie side by side, so the accesses coalesce.
 template <int kKind>
 __device__ __noinline__ void step_block_any(const AdTensor& T, int64_t blk, int lane, const Consts& c) {
   using K = Kind<kKind>;
@@ -234,56 +273,72 @@ __device__ __noinline__ void step_block_any(const AdTensor& T, int64_t blk, int 
   const bool ws = T.flags & kAdWStride, gst = T.flags & kAdGStride;
   const float lr = c.lr * T.lr_scale, step = lr * c.ic1, decay = lr * T.wd;
   const uint32_t sc = K::eight ? *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk) : 0u;
-  float m8[8], r8[8];
+  const int64_t first = blk * kAdBlock + (K::eight ? lane * 8 : lane);
+  constexpr int per = K::eight ? 1 : 32;
+  float m[8], r[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int64_t e = blk * kAdBlock + (K::eight ? lane * 8 + k : lane + 32 * k);
-    float m = 0.f, r = 0.f;
-    if (e < n) {
-      const int64_t wo = ws ? strided(e, T.cols, T.w_ld) : e, go = gst ? strided(e, T.cols, T.g_ld) : e;
-      float v;
-      if (K::eight) {
-        m = __fmul_rn(decode1(reinterpret_cast<const uint8_t*>(T.m)[e]), scale_of(sc & 255u));
-        v = __fmul_rn(decode1(reinterpret_cast<const uint8_t*>(T.v)[e]), scale_of(sc >> 8));
-        v = __fmul_rn(v, v);
-      } else {
-        m = reinterpret_cast<const float*>(T.m)[e];
-        v = reinterpret_cast<const float*>(T.v)[e];
-      }
-      const float g = __fmul_rn(c.gs, to_f32(reinterpret_cast<const GT*>(T.g)[go]));
-      m = __fadd_rn(__fmul_rn(c.b1, m), __fmul_rn(c.c1, g));
-      v = __fadd_rn(__fmul_rn(c.b2, v), __fmul_rn(c.c2, __fmul_rn(g, g)));
-      r = __fsqrt_rn(v);
-      WT* w = reinterpret_cast<WT*>(T.w) + wo;
-      const float x = weight_step(K::master ? T.master[e] : to_f32(*w), m, r, decay, step, c);
-      if (K::master) T.master[e] = x;
-      put(w, x);
-      if (!K::eight) {
-        reinterpret_cast<float*>(T.m)[e] = m;
-        reinterpret_cast<float*>(T.v)[e] = v;
+  for (int k0 = 0; k0 < 8; k0 += 4) {  // four entries' loads before the first use
+    float w[4], g[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j;
+      const int64_t e = first + k * per;
+      w[j] = g[j] = m[k] = r[k] = 0.f;
+      if (e < n) {
+        g[j] = to_f32(reinterpret_cast<const GT*>(T.g)[gst ? strided(e, T.cols, T.g_ld) : e]);
+        w[j] = K::master ? T.master[e] : to_f32(reinterpret_cast<const WT*>(T.w)[ws ? strided(e, T.cols, T.w_ld) : e]);
+        if (K::eight) {
+          m[k] = decode1(reinterpret_cast<const uint8_t*>(T.m)[e]);
+          r[k] = decode1(reinterpret_cast<const uint8_t*>(T.v)[e]);
+        } else {
+          m[k] = reinterpret_cast<const float*>(T.m)[e];
+          r[k] = reinterpret_cast<const float*>(T.v)[e];
+        }
       }
     }
-    m8[k] = m;  // zero past a short last block
-    r8[k] = r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j;
+      const int64_t e = first + k * per;
+      if (K::eight) {
+        m[k] = __fmul_rn(m[k], scale_of(sc & 255u));
+        r[k] = __fmul_rn(r[k], scale_of(sc >> 8));
+        r[k] = __fmul_rn(r[k], r[k]);
+      }
+      const float x = __fmul_rn(c.gs, g[j]);
+      m[k] = __fadd_rn(__fmul_rn(c.b1, m[k]), __fmul_rn(c.c1, x));
+      const float v = __fadd_rn(__fmul_rn(c.b2, r[k]), __fmul_rn(c.c2, __fmul_rn(x, x)));
+      r[k] = __fsqrt_rn(v);
+      if (e < n) {
+        w[j] = weight_step(w[j], m[k], r[k], decay, step, c);
+        if (K::master) T.master[e] = w[j];
+        put(reinterpret_cast<WT*>(T.w) + (ws ? strided(e, T.cols, T.w_ld) : e), w[j]);
+        if (!K::eight) {
+          reinterpret_cast<float*>(T.m)[e] = m[k];
+          reinterpret_cast<float*>(T.v)[e] = v;
+        }
+      } else {
+        m[k] = r[k] = 0.f;  // past a short last block
+      }
+    }
   }
   if (K::eight) {
     const int64_t e0 = blk * kAdBlock + lane * 8;
-    const uint32_t bm = block_exponent(m8), br = block_exponent(r8);
+    const uint32_t bm = block_exponent(m), br = block_exponent(r);
     const uint64_t grp = (uint64_t)e0 >> 3;
     const uint4 rnd = crng::philox4x32_10(make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), c.t, 1u), c.seed, T.id);
-    store_codes(reinterpret_cast<uint8_t*>(T.m), e0, n, false, encode8<true>(m8, bm, rnd));
-    store_codes(reinterpret_cast<uint8_t*>(T.v), e0, n, false, encode8<true>(r8, br, rnd));
+    store_codes(reinterpret_cast<uint8_t*>(T.m), e0, n, false, encode8<true>(m, bm, rnd));
+    store_codes(reinterpret_cast<uint8_t*>(T.v), e0, n, false, encode8<true>(r, br, rnd));
     if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
   }
 }
 
-// A whole block with vector operands, float32 moments.
+// Eight entries of a lane, float32 moments, vector operands.
 template <int kKind>
-__device__ __forceinline__ void step_block32(const AdTensor& T, int64_t blk, int lane, const Consts& c) {
+__device__ __forceinline__ void step_lane32(const AdTensor& T, int64_t e0, const Consts& c) {
   using K = Kind<kKind>;
   using WT = typename K::W;
   using GT = typename K::G;
-  const int64_t e0 = blk * kAdBlock + lane * 8;
   const int64_t wo = T.flags & kAdWStride ? strided(e0, T.cols, T.w_ld) : e0;
   const int64_t go = T.flags & kAdGStride ? strided(e0, T.cols, T.g_ld) : e0;
   float g[8], w[8], m[8], v[8];
@@ -435,16 +490,20 @@ __device__ __forceinline__ void copy_operand(uint32_t dst, const void* base, int
 #pragma unroll
   for (int k = 0; k < kAdTile * (int)sizeof(E); k += 512) copy16(dst + lane16 + k, src + k);
 }
-// the first `entries` entries of a tile of an operand that may have a row stride
+// the same where the tensor ends inside the tile (zeros past its end) or the operand has a row stride
 template <class E>
-__device__ __noinline__ void copy_rows(uint32_t dst, const void* base, int64_t e0, int entries, int lane, int32_t cols, int64_t ld) {
+__device__ __noinline__ void copy_rows(uint32_t dst, const E* base, int64_t e0, int64_t n, int lane, int32_t cols, int64_t ld) {
   constexpr int per = 16 / sizeof(E);
 #pragma unroll 1
-  for (int k = lane * per; k < entries; k += 32 * per)
-    copy16(dst + k * (int)sizeof(E), reinterpret_cast<const E*>(base) + strided(e0 + k, cols, ld));
+  for (int k = lane * per; k < kAdTile; k += 32 * per) {
+    const int64_t e = e0 + k, left = n - e;
+    const int bytes = left >= per ? 16 : left > 0 ? (int)left * (int)sizeof(E) : 0;
+    const E* const src = base + (bytes == 0 ? 0 : cols ? strided(e, cols, ld) : e);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * (int)sizeof(E)), "l"(src), "r"(bytes) : "memory");
+  }
 }
 
-// starts the copies of a tile's whole blocks; returns the lane's block's exponent bytes
+// starts the copies of a tile; returns the exponent bytes of the lane's block
 template <int kKind>
 __device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int lane, uint32_t stage) {
   using L = Stage<kKind>;
@@ -460,19 +519,16 @@ __device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int
     copy_operand<ST>(stage + L::w, w, tile, lane16);
     return reinterpret_cast<const uint16_t*>(T.scales)[2 * (int64_t)tile + (lane >> 4)];
   }
-  const int64_t e0 = (int64_t)tile * kAdTile, whole = T.n / kAdBlock - 2 * (int64_t)tile;
-  if (!(T.flags & kAdVec) || whole < 1) return 0;
-  const int entries = whole > 1 ? kAdTile : kAdBlock;
-  const bool ws = !K::master && (T.flags & kAdWStride), gst = T.flags & kAdGStride;  // without a stride: one row
-  copy_rows<GT>(stage + L::g, reinterpret_cast<const GT*>(T.g) + (gst ? 0 : e0), gst ? e0 : 0, entries, lane, gst ? T.cols : kAdTile, T.g_ld);
-  copy_rows<ST>(stage + L::w, reinterpret_cast<const ST*>(w) + (ws ? 0 : e0), ws ? e0 : 0, entries, lane, ws ? T.cols : kAdTile, T.w_ld);
-  copy_rows<uint8_t>(stage + L::m, reinterpret_cast<const uint8_t*>(T.m) + e0, 0, entries, lane, kAdTile, 0);
-  copy_rows<uint8_t>(stage + L::v, reinterpret_cast<const uint8_t*>(T.v) + e0, 0, entries, lane, kAdTile, 0);
-  return reinterpret_cast<const uint16_t*>(T.scales)[2 * (int64_t)tile + (whole > 1 && lane >= 16)];
+  if (!(T.flags & kAdVec)) return 0;
+  const int64_t e0 = (int64_t)tile * kAdTile, n = T.n, blk = 2 * (int64_t)tile + (lane >> 4);
+  copy_rows(stage + L::g, reinterpret_cast<const GT*>(T.g), e0, n, lane, T.flags & kAdGStride ? T.cols : 0, T.g_ld);
+  copy_rows(stage + L::w, reinterpret_cast<const ST*>(w), e0, n, lane, !K::master && (T.flags & kAdWStride) ? T.cols : 0, T.w_ld);
+  copy_rows(stage + L::m, reinterpret_cast<const uint8_t*>(T.m), e0, n, lane, 0, 0);
+  copy_rows(stage + L::v, reinterpret_cast<const uint8_t*>(T.v), e0, n, lane, 0, 0);
+  return blk * kAdBlock < n ? reinterpret_cast<const uint16_t*>(T.scales)[blk] : 0u;
 }
 
-// The whole blocks of a tile with vector operands, 8-bit moments, a block to each half of the warp (sixteen entries a
-// lane: what a block costs beside its entries is then paid once for two): the same values as step_block_any with fewer
+// A tile with vector operands, 8-bit moments, a block to each half of the warp (sixteen entries a lane: what a block costs beside its entries is then paid once for two): the same values as step_block_any with fewer
 // instructions, which are what bounds it.
 //  - b1 m = (b1 2^k) code and b2 v = (b2 2^2k) code^2: a power of two commutes with the rounding, so the factor is
 //    formed once a block (while it is a normal number).
@@ -488,9 +544,8 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   using L = Stage<kKind>;
   using WT = typename K::W;
   const bool upper = lane >= 16;
-  const bool on = (2 * (int64_t)tile + upper + 1) * kAdBlock <= T.n;  // else the upper half repeats the lower one's block and stores nothing
-  const int at = (on ? lane : lane - 16) * 16;
-  const int64_t e0 = (int64_t)tile * kAdTile + at;
+  const int at = lane * 16;
+  const int64_t e0 = (int64_t)tile * kAdTile + at;  // entries past the tensor's end are zeros
   float m[16], v[16];
   {
     Raw16<typename K::G> g;
@@ -553,24 +608,42 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
       orr[(k >> 2) + 1] = x.y;
     }
   }
-  if (!on) return true;
+  if (e0 >= T.n) return true;
+  if ((lane & 15) == 0) reinterpret_cast<uint16_t*>(T.scales)[2 * (int64_t)tile + upper] = (uint16_t)(bm | br << 8);
   WT* const pw = reinterpret_cast<WT*>(T.w) + (T.flags & kAdWStride ? strided(e0, T.cols, T.w_ld) : e0);
-  if constexpr (K::master) {
-    w.store(T.master + e0);
-    Raw16<WT> b;
+  uint8_t *const pm = reinterpret_cast<uint8_t*>(T.m) + e0, *const pr = reinterpret_cast<uint8_t*>(T.v) + e0;
+  if (e0 + 16 <= T.n) {
+    if constexpr (K::master) {
+      w.store(T.master + e0);
+      Raw16<WT> b;
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        float x, y;
+        split(w.pair(k), x, y);
+        b.put(k, x, y);
+      }
+      b.store(pw);
+    } else {
+      w.store(pw);
+    }
+    *reinterpret_cast<uint4*>(pm) = make_uint4(om[0], om[1], om[2], om[3]);
+    *reinterpret_cast<uint4*>(pr) = make_uint4(orr[0], orr[1], orr[2], orr[3]);
+  } else {  // the lane with the tensor's last entries
+    const int left = (int)(T.n - e0);
 #pragma unroll
     for (int k = 0; k < 16; k += 2) {
-      float x, y;
-      split(w.pair(k), x, y);
-      b.put(k, x, y);
+      float x[2];
+      split(w.pair(k), x[0], x[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (k + j < left) {
+          if constexpr (K::master) T.master[e0 + k + j] = x[j];
+          put(pw + k + j, x[j]);
+          pm[k + j] = (uint8_t)(om[k >> 2] >> (8 * ((k + j) & 3)));
+          pr[k + j] = (uint8_t)(orr[k >> 2] >> (8 * ((k + j) & 3)));
+        }
     }
-    b.store(pw);
-  } else {
-    w.store(pw);
   }
-  *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(T.m) + e0) = make_uint4(om[0], om[1], om[2], om[3]);
-  *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(T.v) + e0) = make_uint4(orr[0], orr[1], orr[2], orr[3]);
-  if ((lane & 15) == 0) reinterpret_cast<uint16_t*>(T.scales)[2 * (int64_t)tile + upper] = (uint16_t)(bm | br << 8);
   return true;
 }
 
@@ -598,230 +671,349 @@ __device__ __forceinline__ Consts consts_of(const AdHyper& h) {
   return c;
 }
 
-// a warp's walk over the tiles of a launch
-template <int kCap>
-struct Walk {
-  int b, li, end;  // tile, its tensor, the first tile after that tensor
-  __device__ __forceinline__ bool seek(const AdTable<kCap>& tb) {
-    if (b >= tb.total_tiles) return false;
-    if (b >= end) {
-      li = tensor_of(tb, b, li);
-      end = li + 1 < tb.n_tensors ? tb.t[li + 1].tile_begin : tb.total_tiles;
-    }
-    return true;
-  }
-};
-
 }  // namespace
 
-template <int kKind, int kCap>
-__global__ void __launch_bounds__(256, 4) k_adamw32(const __grid_constant__ AdTable<kCap> tb, const __grid_constant__ AdHyper h) {
+// A warp takes one tile and ends: a grid of as many CTAs as that needs moved 98% of the copy rate on the 774M-entry case
+// (3.38 ms), a grid of resident CTAs that walk on 89 to 93% (3.56 to 3.73 ms): its warps load and store in step.
+constexpr int kAd32Warps = 4;
+template <int kKind, class Table>
+__global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_constant__ Table tb, const __grid_constant__ AdHyper h) {
+  __shared__ AdTensor slots[kAd32Warps][2];
   if (h.skip && *h.skip) return;
   const Consts c = consts_of(h);
   const int lane = threadIdx.x & 31;
-  Walk<kCap> at{(int)(blockIdx.x * 8 + (threadIdx.x >> 5)), 0, 0};
-  for (; at.seek(tb); at.b += gridDim.x * 8) {
-    const AdTensor& T = tb.t[at.li];
+  AdTensor* const mine = slots[threadIdx.x >> 5];
+  Walk<Table> at((int)(blockIdx.x * kAd32Warps + (threadIdx.x >> 5)), tb.total_tiles);
+  for (; at.seek(tb, mine); at.b += gridDim.x * kAd32Warps) {
+    const AdTensor& T = tensor_at(tb, at.li, mine, at.which);
     const int64_t tile = at.b - T.tile_begin, blocks = (T.n + kAdBlock - 1) / kAdBlock - 2 * tile;
     for (int k = 0; k < 2 && k < blocks; ++k) {
       const int64_t blk = 2 * tile + k;
-      if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) step_block32<kKind>(T, blk, lane, c);
+      if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) step_lane32<kKind>(T, blk * kAdBlock + lane * 8, c);
       else step_block_any<kKind>(T, blk, lane, c);
     }
   }
 }
 
 // Each warp has two stages of its own: the next tile's operands are on their way into one (cp.async) while the other is
-// stepped. Deeper rings (up to four stages) and five or six CTAs an SM measured the same or slower: the pipes of the
+// stepped. A CTA walks over a stretch of its own: tiles dealt out in turn over the grid took 2.35 ms instead of 2.20 on
+// the 774M-entry case with master (all CTAs load and store in step). Deeper rings (up to four stages) and five or six CTAs an SM measured the same or slower: the pipes of the
 // arithmetic, not the loads, are what is left.
 constexpr int kAd8Warps = 4, kAd8Ctas = 4;
-template <int kKind, int kCap>
-__global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __grid_constant__ AdTable<kCap> tb,
+template <int kKind, class Table>
+__global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __grid_constant__ Table tb,
                                                                      const __grid_constant__ AdHyper h) {
   using L = Stage<kKind>;
   extern __shared__ __align__(16) char smem[];
+  __shared__ AdTensor slots[kAd8Warps][2];
   if (h.skip && *h.skip) return;
   const Consts c = consts_of(h);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, stride = gridDim.x * kAd8Warps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   char* const ring = smem + warp * 2 * L::bytes;
   const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
-  Walk<kCap> next{(int)(blockIdx.x * kAd8Warps + warp), 0, 0};
-  bool more = next.seek(tb);
+  AdTensor* const mine = slots[warp];
+  const int first = (int)((int64_t)tb.total_tiles * blockIdx.x / gridDim.x);
+  Walk<Table> next(first + warp, (int)((int64_t)tb.total_tiles * (blockIdx.x + 1) / gridDim.x));
+  bool more = next.seek(tb, mine);
   uint32_t sc_next = 0;
-  if (more) sc_next = fetch_tile8<kKind>(tb.t[next.li], next.b - tb.t[next.li].tile_begin, lane, ring_addr);
+  if (more) {
+    const AdTensor& N = tensor_at(tb, next.li, mine, next.which);
+    sc_next = fetch_tile8<kKind>(N, next.b - N.tile_begin, lane, ring_addr);
+  }
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (int turn = 0; more; turn ^= 1) {
-    const AdTensor& T = tb.t[next.li];
+    const AdTensor& T = tensor_at(tb, next.li, mine, next.which);
     const int tile = next.b - T.tile_begin;
-    const int64_t whole = T.n / kAdBlock - 2 * (int64_t)tile;
     const uint32_t sc = sc_next;
-    next.b += stride;
-    more = next.seek(tb);
+    next.b += kAd8Warps;
+    more = next.seek(tb, mine);
     __syncwarp();  // every lane has read the stage that is filled now
-    if (more)
-      sc_next = fetch_tile8<kKind>(tb.t[next.li], next.b - tb.t[next.li].tile_begin, lane, ring_addr + (turn ^ 1) * L::bytes);
+    if (more) {
+      const AdTensor& N = tensor_at(tb, next.li, mine, next.which);
+      sc_next = fetch_tile8<kKind>(N, next.b - N.tile_begin, lane, ring_addr + (turn ^ 1) * L::bytes);
+    }
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
     __syncwarp();
-    int k = 0;  // the tile's first block that is not done
-    if ((T.flags & kAdVec) && whole > 0 && step_tile8<kKind>(T, tile, lane, c, h, ring + turn * L::bytes, sc))
-      k = whole > 1 ? 2 : 1;
-    for (; k < 2 && (2 * (int64_t)tile + k) * kAdBlock < T.n; ++k) step_block_any<kKind>(T, 2 * (int64_t)tile + k, lane, c);
+    if ((T.flags & kAdVec) && step_tile8<kKind>(T, tile, lane, c, h, ring + turn * L::bytes, sc)) continue;
+    for (int k = 0; k < 2 && (2 * (int64_t)tile + k) * kAdBlock < T.n; ++k) step_block_any<kKind>(T, 2 * (int64_t)tile + k, lane, c);
   }
 }
 
 namespace {
-template <int kKind, int kCap>
-cudaError_t launch_kind(const AdTable<kCap>& tb, const AdHyper& h, int sms, cudaStream_t s) {
+template <int kKind, class Table>
+cudaError_t launch_kind(const Table& tb, const AdHyper& h, int sms, cudaStream_t s) {
   if constexpr (Kind<kKind>::eight) {
     const int want = (tb.total_tiles + kAd8Warps - 1) / kAd8Warps;
     const int grid = want < 1 ? 1 : (want < sms * kAd8Ctas ? want : sms * kAd8Ctas);
-    k_adamw8<kKind, kCap><<<grid, 32 * kAd8Warps, kAd8Warps * 2 * Stage<kKind>::bytes, s>>>(tb, h);
+    k_adamw8<kKind, Table><<<grid, 32 * kAd8Warps, kAd8Warps * 2 * Stage<kKind>::bytes, s>>>(tb, h);
   } else {
-    const int want = (tb.total_tiles + 7) / 8;
-    const int grid = want < 1 ? 1 : (want < sms * 8 ? want : sms * 8);
-    k_adamw32<kKind, kCap><<<grid, 256, 0, s>>>(tb, h);
+    const int want = (tb.total_tiles + kAd32Warps - 1) / kAd32Warps;
+    k_adamw32<kKind, Table><<<want < 1 ? 1 : want, 32 * kAd32Warps, 0, s>>>(tb, h);
   }
   return cudaGetLastError();
 }
 }  // namespace
 
-template <int kCap>
-cudaError_t launch_adamw(int kind, const AdTable<kCap>& tb, const AdHyper& h, int sms, cudaStream_t s) {
+template <class Table>
+cudaError_t launch_adamw(int kind, const Table& tb, const AdHyper& h, int sms, cudaStream_t s) {
   switch (kind) {
-    case AD_W_F32: return launch_kind<AD_W_F32, kCap>(tb, h, sms, s);
-    case AD_W_BF16: return launch_kind<AD_W_BF16, kCap>(tb, h, sms, s);
-    case AD_W_MASTER: return launch_kind<AD_W_MASTER, kCap>(tb, h, sms, s);
-    case AD_W_F32 | AD_G_BF16: return launch_kind<AD_W_F32 | AD_G_BF16, kCap>(tb, h, sms, s);
-    case AD_W_BF16 | AD_G_BF16: return launch_kind<AD_W_BF16 | AD_G_BF16, kCap>(tb, h, sms, s);
-    case AD_W_MASTER | AD_G_BF16: return launch_kind<AD_W_MASTER | AD_G_BF16, kCap>(tb, h, sms, s);
-    case AD_W_F32 | AD_8BIT: return launch_kind<AD_W_F32 | AD_8BIT, kCap>(tb, h, sms, s);
-    case AD_W_BF16 | AD_8BIT: return launch_kind<AD_W_BF16 | AD_8BIT, kCap>(tb, h, sms, s);
-    case AD_W_MASTER | AD_8BIT: return launch_kind<AD_W_MASTER | AD_8BIT, kCap>(tb, h, sms, s);
-    case AD_W_F32 | AD_G_BF16 | AD_8BIT: return launch_kind<AD_W_F32 | AD_G_BF16 | AD_8BIT, kCap>(tb, h, sms, s);
-    case AD_W_BF16 | AD_G_BF16 | AD_8BIT: return launch_kind<AD_W_BF16 | AD_G_BF16 | AD_8BIT, kCap>(tb, h, sms, s);
-    case AD_W_MASTER | AD_G_BF16 | AD_8BIT: return launch_kind<AD_W_MASTER | AD_G_BF16 | AD_8BIT, kCap>(tb, h, sms, s);
+    case AD_W_F32: return launch_kind<AD_W_F32, Table>(tb, h, sms, s);
+    case AD_W_BF16: return launch_kind<AD_W_BF16, Table>(tb, h, sms, s);
+    case AD_W_MASTER: return launch_kind<AD_W_MASTER, Table>(tb, h, sms, s);
+    case AD_W_F32 | AD_G_BF16: return launch_kind<AD_W_F32 | AD_G_BF16, Table>(tb, h, sms, s);
+    case AD_W_BF16 | AD_G_BF16: return launch_kind<AD_W_BF16 | AD_G_BF16, Table>(tb, h, sms, s);
+    case AD_W_MASTER | AD_G_BF16: return launch_kind<AD_W_MASTER | AD_G_BF16, Table>(tb, h, sms, s);
+    case AD_W_F32 | AD_8BIT: return launch_kind<AD_W_F32 | AD_8BIT, Table>(tb, h, sms, s);
+    case AD_W_BF16 | AD_8BIT: return launch_kind<AD_W_BF16 | AD_8BIT, Table>(tb, h, sms, s);
+    case AD_W_MASTER | AD_8BIT: return launch_kind<AD_W_MASTER | AD_8BIT, Table>(tb, h, sms, s);
+    case AD_W_F32 | AD_G_BF16 | AD_8BIT: return launch_kind<AD_W_F32 | AD_G_BF16 | AD_8BIT, Table>(tb, h, sms, s);
+    case AD_W_BF16 | AD_G_BF16 | AD_8BIT: return launch_kind<AD_W_BF16 | AD_G_BF16 | AD_8BIT, Table>(tb, h, sms, s);
+    case AD_W_MASTER | AD_G_BF16 | AD_8BIT: return launch_kind<AD_W_MASTER | AD_G_BF16 | AD_8BIT, Table>(tb, h, sms, s);
     default: return cudaErrorInvalidValue;
   }
 }
-template cudaError_t launch_adamw<kAdFew>(int, const AdTable<kAdFew>&, const AdHyper&, int, cudaStream_t);
-template cudaError_t launch_adamw<kAdMany>(int, const AdTable<kAdMany>&, const AdHyper&, int, cudaStream_t);
+template cudaError_t launch_adamw(int, const AdTable<kAdFew>&, const AdHyper&, int, cudaStream_t);
+template cudaError_t launch_adamw(int, const AdTable<kAdMany>&, const AdHyper&, int, cudaStream_t);
+template cudaError_t launch_adamw(int, const AdDevTable&, const AdHyper&, int, cudaStream_t);
 
 // ---------------------------------------------------------------- gradient norm
-// Sum of squares of a lane's eight entries in float32, added up in float64 in a fixed order. Where the
-// float32 sum leaves [2^-90, 2^120] (squares that underflow or overflow, NaN, zeros) it is formed in
-// float64 instead, so every finite gradient has its norm.
-__global__ void __launch_bounds__(256) k_grad_sumsq(const __grid_constant__ NormTable tb) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double acc = 0.0;
-  int li = 0, end = 0;
-  for (int b = blockIdx.x * 8 + warp; b < tb.total_blocks; b += gridDim.x * 8) {
-    if (b >= end) {
-      li = tensor_of(tb, b, li);
-      end = li + 1 < tb.n_tensors ? tb.t[li + 1].block_begin : tb.total_blocks;
-    }
-    const NormTensor& T = tb.t[li];
-    const int64_t n = T.n, e0 = (int64_t)(b - T.block_begin) * kAdBlock + lane * 8;
-    const bool vec = T.vec && e0 + 8 <= n, st = T.ld != T.cols;
-    float g[8];
-    if (T.bf16) load(reinterpret_cast<const __nv_bfloat16*>(T.g), e0, n, T.cols, T.ld, st, vec, g);
-    else load(reinterpret_cast<const float*>(T.g), e0, n, T.cols, T.ld, st, vec, g);
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s = fmaf(g[k], g[k], s);
-    double d = (double)s;
-    if (!(s >= 0x1p-90f && s <= 0x1p120f)) {
-      d = 0.0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) d = fma((double)g[k], (double)g[k], d);
-    }
-    acc += d;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  __shared__ double part[8];
-  if (lane == 0) part[warp] = acc;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int k = 0; k < 8; ++k) s += part[k];
-    tb.partials[blockIdx.x] = s;
-  }
+// A lane squares eight entries at a time: their sum in float32 (one rounding an entry), added up in float64 in a fixed
+// order. Where the float32 sum leaves [2^-90, 2^120] (squares that underflow or overflow, NaN, zeros) it is formed in
+// float64 instead, so every gradient whose norm float32 holds gets it.
+namespace {
+constexpr float kNormLow = 0x1p-90f, kNormHigh = 0x1p120f;
+__device__ __noinline__ double sumsq_f64(const float (&g)[8]) {
+  double d = 0.0;
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) d = fma((double)g[k], (double)g[k], d);
+  return d;
 }
 
-__global__ void __launch_bounds__(256) k_grad_norm_finish(const __grid_constant__ NormOut o) {
-  __shared__ double part[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double acc = 0.0;
-  for (int i = threadIdx.x; i < o.n_partials; i += 256) acc += o.partials[i];
+template <class E>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  uint32_t u[8];
+  __device__ __forceinline__ void load(const float* p) { ld256(p, u); }
+  __device__ __forceinline__ float sum() const {
+    F2 a{0};
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
-  if (lane == 0) part[warp] = acc;
+    for (int k = 0; k < 8; k += 2) {
+      const F2 x = two(__uint_as_float(u[k]), __uint_as_float(u[k + 1]));
+      a = k ? fma2(x, x, a) : mul2(x, x);
+    }
+    float lo, hi;
+    split(a, lo, hi);
+    return __fadd_rn(lo, hi);
+  }
+  __device__ __forceinline__ void values(float (&g)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = __uint_as_float(u[k]);
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+  }
+  __device__ __forceinline__ float sum() const {  // bf16 factors, float32 sum: nothing to unpack
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      asm("fma.rn.f32.bf16 %0, %1, %1, %0;" : "+f"(s) : "h"((uint16_t)u[k]));
+      asm("fma.rn.f32.bf16 %0, %1, %1, %0;" : "+f"(s) : "h"((uint16_t)(u[k] >> 16)));
+    }
+    return s;
+  }
+  __device__ __forceinline__ void values(float (&g)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      g[2 * k] = __uint_as_float(u[k] << 16);
+      g[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+  }
+};
+template <class E>
+__device__ __forceinline__ double sumsq(const Raw8<E>& x) {
+  const float s = x.sum();
+  if (s >= kNormLow && s <= kNormHigh) return (double)s;
+  uint32_t any = 0;  // rows without a gradient are common: no float64 for them
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(x.u) / 4); ++k) any |= x.u[k];
+  if (any == 0) return 0.0;
+  float g[8];
+  x.values(g);
+  return sumsq_f64(g);
+}
+
+// what a warp keeps of the tensor it is in
+struct NormAt {
+  const void* g;
+  int64_t n;
+  int begin;
+  bool fast;  // contiguous and aligned
+};
+
+// tile of 1,024 entries: four loads of eight a lane under way at once
+template <class E>
+__device__ __forceinline__ double tile_sumsq(const NormAt& A, const NormTensor& T, int tile, int lane) {
+  const E* const p = reinterpret_cast<const E*>(A.g);
+  const int64_t e0 = (int64_t)tile * kNormTile + lane * 8;
+  double d = 0.0;
+  if (A.fast && (int64_t)(tile + 1) * kNormTile <= A.n) {
+    Raw8<E> x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k].load(p + e0 + k * kAdBlock);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d += sumsq(x[k]);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const int64_t e = e0 + k * kAdBlock;
+      if (e >= A.n) break;
+      const bool stride = T.ld != T.cols;
+      if (T.vec && e + 8 <= A.n) {
+        Raw8<E> x;
+        x.load(p + (stride ? strided(e, T.cols, T.ld) : e));
+        d += sumsq(x);
+      } else {
+        float g[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = e + j < A.n ? to_f32(p[stride ? strided(e + j, T.cols, T.ld) : e + j]) : 0.f;
+        d += sumsq_f64(g);
+      }
+    }
+  }
+  return d;
+}
+
+// sum over the CTA, in a fixed order, in thread 0
+__device__ __forceinline__ double cta_sum(double acc) {
+  __shared__ double part[8];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = acc;
   __syncthreads();
-  if (threadIdx.x) return;
   double s = 0.0;
-  for (int k = 0; k < 8; ++k) s += part[k];
+  if (threadIdx.x == 0)
+    for (int k = 0; k < 8; ++k) s += part[k];
+  return s;
+}
+}  // namespace
+
+__global__ void __launch_bounds__(256, 4) k_grad_norm(const __grid_constant__ NormArgs a) {
+  const int lane = threadIdx.x & 31;
+  double acc = 0.0;
+  int li = 0, end = 0;
+  NormAt A{};
+  bool bf16 = false;
+  for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < a.total_tiles; b += gridDim.x * 8) {
+    if (b >= end) {
+      li = tensor_of_warp(a.t, a.n_tensors, b, li);
+      const NormTensor& T = a.t[li];
+      A = NormAt{T.g, T.n, T.tile_begin, T.vec && T.ld == T.cols};
+      bf16 = T.bf16;
+      end = li + 1 < a.n_tensors ? a.t[li + 1].tile_begin : a.total_tiles;
+    }
+    acc += bf16 ? tile_sumsq<__nv_bfloat16>(A, a.t[li], b - A.begin, lane) : tile_sumsq<float>(A, a.t[li], b - A.begin, lane);
+  }
+  const double mine = cta_sum(acc);
+  __shared__ bool last;
+  if (threadIdx.x == 0) {
+    a.partials[blockIdx.x] = mine;
+    __threadfence();
+    last = atomicInc(a.arrived, gridDim.x - 1) == gridDim.x - 1;  // wraps to zero for the next launch
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  acc = 0.0;
+#pragma unroll
+  for (int k = 0; k < (kNormMaxGrid + 255) / 256; ++k) {
+    const int i = threadIdx.x + 256 * k;
+    if (i < gridDim.x) acc += *(volatile double*)(a.partials + i);
+  }
+  const double s = cta_sum(acc);
+  if (threadIdx.x) return;
   const double norm = sqrt(s);
   const float f = (float)norm;
   const bool bad = !(f <= 3.402823466e38f);
-  o.out[0] = f;
-  o.out[1] = bad ? 0.f : (float)fmin(1.0, o.max_norm / (norm + 1e-6));
-  if (o.skip) *o.skip = bad;
-  if (o.status && bad) atomicOr(o.status, SMUON_DEV_NONFINITE_NORM);
+  a.out[0] = f;
+  a.out[1] = bad ? 0.f : (float)fmin(1.0, a.max_norm / (norm + 1e-6));
+  if (a.skip) *a.skip = bad;
+  if (a.status && bad) atomicOr(a.status, SMUON_DEV_NONFINITE_NORM);
 }
 
-int norm_grid(int total_blocks) {
-  const int want = (total_blocks + 7) / 8;
-  return want < 1 ? 1 : (want < kNormMaxGrid ? want : kNormMaxGrid);
-}
-
-cudaError_t launch_grad_norm(const NormTable& tb, cudaStream_t s) {
-  k_grad_sumsq<<<norm_grid(tb.total_blocks), 256, 0, s>>>(tb);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_grad_norm_finish(const NormOut& o, cudaStream_t s) {
-  k_grad_norm_finish<<<1, 256, 0, s>>>(o);
+cudaError_t launch_grad_norm(const NormArgs& a, cudaStream_t s) {
+  const int want = (a.total_tiles + 7) / 8;
+  k_grad_norm<<<want < 1 ? 1 : (want < kNormMaxGrid ? want : kNormMaxGrid), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- conversion
+// A warp takes a tile of two blocks: the loads of both are under way before either is converted. One tile a warp, as in
+// k_adamw32 (65.6M entries to 32 bits: 102 us; with a grid of resident CTAs 118 us).
+namespace {
+__device__ __forceinline__ void convert_to8(const ConvTensor& T, int64_t blk, int lane, const float (&m)[8], float (&r)[8]) {
+  const int64_t e0 = blk * kAdBlock + lane * 8;
+  const bool vec = T.vec && e0 + 8 <= T.n;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r[k] = __fsqrt_rn(r[k]);
+  const uint32_t bm = block_exponent(m), br = block_exponent(r);
+  store_codes(reinterpret_cast<uint8_t*>(T.m8), e0, T.n, vec, encode8<false>(m, bm, make_uint4(0, 0, 0, 0)));
+  store_codes(reinterpret_cast<uint8_t*>(T.v8), e0, T.n, vec, encode8<false>(r, br, make_uint4(0, 0, 0, 0)));
+  if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
+}
+__device__ __forceinline__ void convert_to32(const ConvTensor& T, int64_t blk, int lane, uint32_t sc, uint2 cm, uint2 cr) {
+  const int64_t e0 = blk * kAdBlock + lane * 8;
+  const bool vec = T.vec && e0 + 8 <= T.n;
+  float m[8], r[8];
+  decode8(cm, scale_of(sc & 255u), m);
+  decode8(cr, scale_of(sc >> 8), r);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r[k] = __fmul_rn(r[k], r[k]);
+  store(reinterpret_cast<float*>(T.m32), e0, T.n, e0, vec, m);
+  store(reinterpret_cast<float*>(T.v32), e0, T.n, e0, vec, r);
+}
+}  // namespace
+
 __global__ void __launch_bounds__(256) k_adamw_convert(const __grid_constant__ ConvTable tb) {
   const int lane = threadIdx.x & 31;
   int li = 0, end = 0;
-  for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < tb.total_blocks; b += gridDim.x * 8) {
+  for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < tb.total_tiles; b += gridDim.x * 8) {
     if (b >= end) {
       li = tensor_of(tb, b, li);
-      end = li + 1 < tb.n_tensors ? tb.t[li + 1].block_begin : tb.total_blocks;
+      end = li + 1 < tb.n_tensors ? tb.t[li + 1].tile_begin : tb.total_tiles;
     }
     const ConvTensor& T = tb.t[li];
-    const int64_t n = T.n, blk = b - T.block_begin, e0 = blk * kAdBlock + lane * 8;
-    const bool vec = T.vec && e0 + 8 <= n;
-    float m[8], r[8];
+    const int64_t n = T.n, blk = 2 * (int64_t)(b - T.tile_begin), e0 = blk * kAdBlock + lane * 8;
+    const bool two_blocks = (blk + 1) * kAdBlock < n;
+    const bool v0 = T.vec && e0 + 8 <= n, v1 = T.vec && e0 + kAdBlock + 8 <= n;
     if (tb.to8) {
-      load(reinterpret_cast<const float*>(T.m32), e0, n, 1, 1, false, vec, m);
-      load(reinterpret_cast<const float*>(T.v32), e0, n, 1, 1, false, vec, r);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] = __fsqrt_rn(r[k]);
-      const uint32_t bm = block_exponent(m), br = block_exponent(r);
-      store_codes(reinterpret_cast<uint8_t*>(T.m8), e0, n, vec, encode8<false>(m, bm, make_uint4(0, 0, 0, 0)));
-      store_codes(reinterpret_cast<uint8_t*>(T.v8), e0, n, vec, encode8<false>(r, br, make_uint4(0, 0, 0, 0)));
-      if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
+      float m0[8], r0[8], m1[8], r1[8];
+      load(reinterpret_cast<const float*>(T.m32), e0, n, e0, v0, m0);
+      load(reinterpret_cast<const float*>(T.v32), e0, n, e0, v0, r0);
+      load(reinterpret_cast<const float*>(T.m32), e0 + kAdBlock, n, e0 + kAdBlock, v1, m1);
+      load(reinterpret_cast<const float*>(T.v32), e0 + kAdBlock, n, e0 + kAdBlock, v1, r1);
+      convert_to8(T, blk, lane, m0, r0);
+      if (two_blocks) convert_to8(T, blk + 1, lane, m1, r1);
     } else {
-      const uint32_t sc = *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk);
-      decode8(load_codes(reinterpret_cast<const uint8_t*>(T.m8), e0, n, vec), scale_of(sc & 255u), m);
-      decode8(load_codes(reinterpret_cast<const uint8_t*>(T.v8), e0, n, vec), scale_of(sc >> 8), r);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] = __fmul_rn(r[k], r[k]);
-      store(reinterpret_cast<float*>(T.m32), e0, n, 1, 1, false, vec, m);
-      store(reinterpret_cast<float*>(T.v32), e0, n, 1, 1, false, vec, r);
+      const uint16_t* const sc = reinterpret_cast<const uint16_t*>(T.scales);
+      const uint8_t *pm = reinterpret_cast<const uint8_t*>(T.m8), *pr = reinterpret_cast<const uint8_t*>(T.v8);
+      const uint32_t s0 = sc[blk], s1 = two_blocks ? sc[blk + 1] : 0u;
+      const uint2 m0 = load_codes(pm, e0, n, v0), r0 = load_codes(pr, e0, n, v0);
+      const uint2 m1 = load_codes(pm, e0 + kAdBlock, n, v1), r1 = load_codes(pr, e0 + kAdBlock, n, v1);
+      convert_to32(T, blk, lane, s0, m0, r0);
+      if (two_blocks) convert_to32(T, blk + 1, lane, s1, m1, r1);
     }
   }
 }
 
-cudaError_t launch_adamw_convert(const ConvTable& tb, int sms, cudaStream_t s) {
-  const int want = (tb.total_blocks + 7) / 8;
-  const int grid = want < 1 ? 1 : (want < sms * 8 ? want : sms * 8);
-  k_adamw_convert<<<grid, 256, 0, s>>>(tb);
+cudaError_t launch_adamw_convert(const ConvTable& tb, cudaStream_t s) {
+  const int want = (tb.total_tiles + 7) / 8;
+  k_adamw_convert<<<want < 1 ? 1 : want, 256, 0, s>>>(tb);
   return cudaGetLastError();
 }
 

@@ -191,8 +191,8 @@ def test_step_and_plan_refuse(L, name):
     assert L.adamw_step(ctypes.byref(st), G, a["lr"], a["beta1"], a["beta2"], a["eps"], None, None, a["skip"], None) == code
     assert word in L.smuon_last_error(), L.smuon_last_error()
     h = ctypes.c_void_p(1)
-    assert L.adamw_plan_create(ctypes.byref(st), G, a["beta1"], a["beta2"], a["eps"], None, None, a["skip"],
-                               ctypes.byref(h)) == code
+    assert L.adamw_plan_create(ctypes.byref(st), G, a["beta1"], a["beta2"], a["eps"], None, None, a["skip"], ADDR * 30,
+                               4096, None, ctypes.byref(h)) == code
     assert not h.value
     assert st.t == st_kw.get("t", 0)
 
@@ -256,19 +256,27 @@ def test_norm_refuses(L):
     assert call(G=_mats(_m(0, dt=S.I8)), n=1) == -3
     assert call(G=_mats(_m(0, ld=3)), n=1) == -2
     h = ctypes.c_void_p(1)
-    assert L.smuon_grad_norm_plan_create(G, 2, -1.0, ADDR * 4, None, ADDR * 5, size.value, None, ctypes.byref(h)) == -1
+    assert L.smuon_grad_norm_plan_create(G, 2, -1.0, ADDR * 4, None, ADDR * 5, size.value, None, None,
+                                         ctypes.byref(h)) == -1
     assert not h.value
 
 
-def test_workspace_holds_one_sum_per_cta(L):
-    """At most 1,184 CTAs a launch, 8 bytes each; 512 tensors a launch; empty tensors need none."""
+def test_workspaces(L):
+    """A norm's holds its table (40 bytes a tensor) and a sum for each of at most 592 CTAs; a step's plan 96 bytes a
+    tensor. A plan refuses one that is missing, misaligned or too small."""
     size = ctypes.c_size_t(0)
-    one = _mats(_m(0, rows=65536, cols=65536))
-    assert L.smuon_grad_norm_workspace_bytes(one, 1, ctypes.byref(size)) == 0 and size.value >= 1184 * 8
-    many = _mats(*[_m(k, rows=1, cols=1) for k in range(1025)])
-    assert L.smuon_grad_norm_workspace_bytes(many, 1025, ctypes.byref(size)) == 0 and size.value >= 3 * 8
+    for n in (1, 512, 5000):
+        G = _mats(*[_m(k, rows=1, cols=1) for k in range(n)])
+        assert L.smuon_grad_norm_workspace_bytes(G, n, ctypes.byref(size)) == 0 and size.value >= 592 * 8 + 40 * n
     none = _mats(S.SmuonMat(None, 0, 5, 5, S.F32))
     assert L.smuon_grad_norm_workspace_bytes(none, 1, ctypes.byref(size)) == 0
+    assert L.smuon_grad_norm_workspace_bytes(none, 1, None) == -1
+    st, h = _state(), ctypes.c_void_p()
+    assert L.adamw_plan_workspace_bytes(ctypes.byref(st), ctypes.byref(size)) == 0 and size.value >= 96
+    assert L.adamw_plan_workspace_bytes(None, ctypes.byref(size)) == -1
+    for ws, n in ((None, 4096), (ADDR * 30 + 16, 4096), (ADDR * 30, 95)):
+        assert L.adamw_plan_create(ctypes.byref(st), _mats(_m(3)), 0.9, 0.999, 1e-8, None, None, None, ws, n, None,
+                                   ctypes.byref(h)) == -5
 
 
 def test_binding_refuses_before_the_library():
