@@ -22,6 +22,28 @@
 namespace smuon {
 namespace {
 
+// ---------------------------------------------------------------- launches
+// These kernels are launched so that they may begin while the kernel before them in the stream ends (programmatic
+// dependent launch): the next one's CTAs are let in at once, and memory is touched only after what came before is done.
+// A chain of small calls takes one launch latency less each.
+__device__ __forceinline__ void follow_previous() {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), int grid, int block, int smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- eight entries of a lane
 __device__ __forceinline__ void ld256(const void* p, uint32_t (&u)[8]) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -647,7 +669,6 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   return true;
 }
 
-// the call's numbers; the last CTA to have read the step count steps it
 __device__ __forceinline__ Consts consts_of(const AdHyper& h) {
   const int64_t t = h.d_t ? *h.d_t + 1 : h.t;
   Consts c;
@@ -658,41 +679,48 @@ __device__ __forceinline__ Consts consts_of(const AdHyper& h) {
   c.ic2 = rsqrtf(-expm1f((float)((double)t * h.log_b2)));
   c.t = (uint32_t)t;
   c.seed = h.seed;
-  if (h.d_t && h.advance) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      if (atomicAdd(reinterpret_cast<unsigned long long*>(h.d_t + 1), 1ull) + 1 == gridDim.x) {
-        h.d_t[1] = 0;
-        h.d_t[0] = t;
-      }
+  return c;
+}
+
+// at a kernel's end, in the call's last launch: the last CTA to come here counts the step
+__device__ __forceinline__ void advance(const AdHyper& h, int skip) {
+  if (!h.d_t || !h.advance || skip) return;
+  __syncthreads();  // every thread of the CTA has read the count
+  if (threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(reinterpret_cast<unsigned long long*>(h.d_t + 1), 1ull) + 1 == gridDim.x) {
+      h.d_t[1] = 0;
+      h.d_t[0] += 1;
     }
   }
-  return c;
 }
 
 }  // namespace
 
-// A warp takes one tile and ends: a grid of as many CTAs as that needs moved 98% of the copy rate on the 774M-entry case
-// (3.38 ms), a grid of resident CTAs that walk on 89 to 93% (3.56 to 3.73 ms): its warps load and store in step.
+// A warp takes one block and ends: a grid of as many CTAs as that needs moved 98% of the copy rate on the 774M-entry
+// case (3.38 ms), a grid of resident CTAs that walk on 89 to 93% (3.56 to 3.73 ms): its warps load and store in step.
 constexpr int kAd32Warps = 4;
 template <int kKind, class Table>
 __global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_constant__ Table tb, const __grid_constant__ AdHyper h) {
   __shared__ AdTensor slots[kAd32Warps][2];
-  if (h.skip && *h.skip) return;
+  follow_previous();
+  const int skip = h.skip ? *h.skip : 0;
   const Consts c = consts_of(h);
   const int lane = threadIdx.x & 31;
+  const unsigned unit = blockIdx.x * kAd32Warps + (threadIdx.x >> 5);  // block of the launch, two for each tile
   AdTensor* const mine = slots[threadIdx.x >> 5];
-  Walk<Table> at((int)(blockIdx.x * kAd32Warps + (threadIdx.x >> 5)), tb.total_tiles);
-  for (; at.seek(tb, mine); at.b += gridDim.x * kAd32Warps) {
+  Walk<Table> at((int)(unit >> 1), tb.total_tiles);
+  if (at.seek(tb, mine)) {
     const AdTensor& T = tensor_at(tb, at.li, mine, at.which);
-    const int64_t tile = at.b - T.tile_begin, blocks = (T.n + kAdBlock - 1) / kAdBlock - 2 * tile;
-    for (int k = 0; k < 2 && k < blocks; ++k) {
-      const int64_t blk = 2 * tile + k;
-      if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) step_lane32<kKind>(T, blk * kAdBlock + lane * 8, c);
-      else step_block_any<kKind>(T, blk, lane, c);
+    const int64_t blk = 2 * (int64_t)(at.b - T.tile_begin) + (unit & 1);
+    if (skip) {
+    } else if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) {
+      step_lane32<kKind>(T, blk * kAdBlock + lane * 8, c);
+    } else if (blk * kAdBlock < T.n) {
+      step_block_any<kKind>(T, blk, lane, c);
     }
   }
+  advance(h, skip);
 }
 
 // Each warp has two stages of its own: the next tile's operands are on their way into one (cp.async) while the other is
@@ -706,7 +734,8 @@ __global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __gri
   using L = Stage<kKind>;
   extern __shared__ __align__(16) char smem[];
   __shared__ AdTensor slots[kAd8Warps][2];
-  if (h.skip && *h.skip) return;
+  follow_previous();
+  const int skip = h.skip ? *h.skip : 0;
   const Consts c = consts_of(h);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   char* const ring = smem + warp * 2 * L::bytes;
@@ -721,6 +750,10 @@ __global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __gri
     sc_next = fetch_tile8<kKind>(N, next.b - N.tile_begin, lane, ring_addr);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
+  if (skip) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    more = false;
+  }
   for (int turn = 0; more; turn ^= 1) {
     const AdTensor& T = tensor_at(tb, next.li, mine, next.which);
     const int tile = next.b - T.tile_begin;
@@ -737,6 +770,7 @@ __global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __gri
     if ((T.flags & kAdVec) && step_tile8<kKind>(T, tile, lane, c, h, ring + turn * L::bytes, sc)) continue;
     for (int k = 0; k < 2 && (2 * (int64_t)tile + k) * kAdBlock < T.n; ++k) step_block_any<kKind>(T, 2 * (int64_t)tile + k, lane, c);
   }
+  advance(h, skip);
 }
 
 namespace {
@@ -745,12 +779,11 @@ cudaError_t launch_kind(const Table& tb, const AdHyper& h, int sms, cudaStream_t
   if constexpr (Kind<kKind>::eight) {
     const int want = (tb.total_tiles + kAd8Warps - 1) / kAd8Warps;
     const int grid = want < 1 ? 1 : (want < sms * kAd8Ctas ? want : sms * kAd8Ctas);
-    k_adamw8<kKind, Table><<<grid, 32 * kAd8Warps, kAd8Warps * 2 * Stage<kKind>::bytes, s>>>(tb, h);
+    return launch(k_adamw8<kKind, Table>, grid, 32 * kAd8Warps, kAd8Warps * 2 * Stage<kKind>::bytes, s, tb, h);
   } else {
-    const int want = (tb.total_tiles + kAd32Warps - 1) / kAd32Warps;
-    k_adamw32<kKind, Table><<<want < 1 ? 1 : want, 32 * kAd32Warps, 0, s>>>(tb, h);
+    const int want = (int)((2 * (int64_t)tb.total_tiles + kAd32Warps - 1) / kAd32Warps);
+    return launch(k_adamw32<kKind, Table>, want < 1 ? 1 : want, 32 * kAd32Warps, 0, s, tb, h);
   }
-  return cudaGetLastError();
 }
 }  // namespace
 
@@ -907,6 +940,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_norm(const __grid_constant__ No
   const int lane = threadIdx.x & 31;
   double acc = 0.0;
   int li = 0, end = 0;
+  follow_previous();
   NormAt A{};
   bool bf16 = false;
   for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < a.total_tiles; b += gridDim.x * 8) {
@@ -948,8 +982,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_norm(const __grid_constant__ No
 
 cudaError_t launch_grad_norm(const NormArgs& a, cudaStream_t s) {
   const int want = (a.total_tiles + 7) / 8;
-  k_grad_norm<<<want < 1 ? 1 : (want < kNormMaxGrid ? want : kNormMaxGrid), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch(k_grad_norm, want < 1 ? 1 : (want < kNormMaxGrid ? want : kNormMaxGrid), 256, 0, s, a);
 }
 
 // ---------------------------------------------------------------- conversion
@@ -980,6 +1013,7 @@ __device__ __forceinline__ void convert_to32(const ConvTensor& T, int64_t blk, i
 }  // namespace
 
 __global__ void __launch_bounds__(256) k_adamw_convert(const __grid_constant__ ConvTable tb) {
+  follow_previous();
   const int lane = threadIdx.x & 31;
   int li = 0, end = 0;
   for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < tb.total_tiles; b += gridDim.x * 8) {
@@ -1013,8 +1047,7 @@ __global__ void __launch_bounds__(256) k_adamw_convert(const __grid_constant__ C
 
 cudaError_t launch_adamw_convert(const ConvTable& tb, cudaStream_t s) {
   const int want = (tb.total_tiles + 7) / 8;
-  k_adamw_convert<<<want < 1 ? 1 : want, 256, 0, s>>>(tb);
-  return cudaGetLastError();
+  return launch(k_adamw_convert, want < 1 ? 1 : want, 256, 0, s, tb);
 }
 
 }  // namespace smuon
