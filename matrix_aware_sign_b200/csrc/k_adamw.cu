@@ -272,8 +272,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return d;
 }
 
-// W' from m' and r' = sqrt(v'); square root and reciprocal are approximations within two units in the last place:
-// the direction is rounded to 2^-24 of W afterwards, which it is a small part of
+// W' from m' and r' = sqrt(v'); the reciprocal is an approximation within a unit in the last place: the direction is a
+// small part of W, which is rounded to 2^-24 of itself afterwards
 __device__ __forceinline__ float weight_step(float w, float m, float r, float decay, float step, const Consts& c) {
   return fmaf(-step, m * rcp_approx(fmaf(r, c.ic2, c.eps)), fmaf(-decay, w, w));  // step = lr / (1 - b1^t), decay = lr wd
 }
@@ -550,8 +550,9 @@ __device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int
   return blk * kAdBlock < n ? reinterpret_cast<const uint16_t*>(T.scales)[blk] : 0u;
 }
 
-// A tile with vector operands, 8-bit moments, a block to each half of the warp (sixteen entries a lane: what a block costs beside its entries is then paid once for two): the same values as step_block_any with fewer
-// instructions, which are what bounds it.
+// A tile with vector operands, 8-bit moments, a block to each half of the warp (sixteen entries a lane: what a block
+// costs beside its entries is then paid once for two): the same values as step_block_any with fewer instructions (370 a warp
+// for 256 entries, the first form took 770), which are what bounds it.
 //  - b1 m = (b1 2^k) code and b2 v = (b2 2^2k) code^2: a power of two commutes with the rounding, so the factor is
 //    formed once a block (while it is a normal number).
 //  - r' only goes into W' and into its code, which depends on r' through the carry out of its 20 low bits. An
@@ -576,7 +577,8 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
     const float sm = scale_of(sc & 255u), sr = scale_of(sc >> 8);
     const float b1s = c.b1 * sm, b2s = c.b2 * (sr * sr);
     // exact factors: zero, or normal with room on both sides
-    const bool ok = (sm == 0.f || (b1s >= 0x1p-100f && b1s <= 0x1p100f)) && (sr == 0.f || (b2s >= 0x1p-100f && b2s <= 0x1p100f));
+    const bool ok = (sm == 0.f || c.b1 == 0.f || (b1s >= 0x1p-100f && b1s <= 0x1p100f)) && sm <= 0x1p100f &&
+                    (sr == 0.f || c.b2 == 0.f || (b2s >= 0x1p-100f && b2s <= 0x1p100f)) && sr <= 0x1p50f;
     if (!__all_sync(0xffffffffu, ok)) return false;
     const uint32_t wm[4] = {cm.x, cm.y, cm.z, cm.w}, wr[4] = {cr.x, cr.y, cr.z, cr.w};
     const F2 gs = both(c.gs), b1 = both(b1s), c1 = two(h.c1_2.x, h.c1_2.y), b2 = both(b2s), c2 = two(h.c2_2.x, h.c2_2.y);
@@ -590,6 +592,12 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   const float tm = half_warp_max(m, upper), tv = half_warp_max(v, upper);
   // finite, and so large (or zero) that the smallest v' which the root does not flush to zero is far below the codes
   if (!__all_sync(0xffffffffu, tm <= 0x1p120f && tv <= 0x1p120f && (tv == 0.f || tv >= 0x1p-80f))) return false;
+  if (c.eps < 0x1p-41f) {  // a root flushed to zero (below 2^-63) would show beside such an eps
+    bool tiny = false;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) tiny |= v[k] > 0.f && v[k] < 0x1p-126f;
+    if (__any_sync(0xffffffffu, tiny)) return false;
+  }
   const uint32_t fm = __float_as_uint(tm) >> 23, fr = __float_as_uint(__fsqrt_rn(tv)) >> 23;
   const uint32_t bm = fm > 7u ? fm - 7u : 0u, br = fr > 7u ? fr - 7u : 0u;
   const F2 um = both(bm ? __uint_as_float((254u - bm) << 23) : 0.f);
@@ -713,7 +721,7 @@ __global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_con
   if (at.seek(tb, mine)) {
     const AdTensor& T = tensor_at(tb, at.li, mine, at.which);
     const int64_t blk = 2 * (int64_t)(at.b - T.tile_begin) + (unit & 1);
-    if (skip) {
+    if (skip) {  // nothing
     } else if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) {
       step_lane32<kKind>(T, blk * kAdBlock + lane * 8, c);
     } else if (blk * kAdBlock < T.n) {
@@ -725,8 +733,9 @@ __global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_con
 
 // Each warp has two stages of its own: the next tile's operands are on their way into one (cp.async) while the other is
 // stepped. A CTA walks over a stretch of its own: tiles dealt out in turn over the grid took 2.35 ms instead of 2.20 on
-// the 774M-entry case with master (all CTAs load and store in step). Deeper rings (up to four stages) and five or six CTAs an SM measured the same or slower: the pipes of the
-// arithmetic, not the loads, are what is left.
+// the 774M-entry case with master (all CTAs load and store in step). Deeper rings (up to four stages: 2.35, 2.47 and 2.51
+// ms with two, three and four) and more warps with fewer registers measured slower. The pipes of the arithmetic are what
+// is left on bf16 weights without a master (issue slots 65% busy, integer pipe 51%, HBM 54%; 65.6M entries: 134 to 141 us).
 constexpr int kAd8Warps = 2, kAd8Ctas = 8;
 constexpr int kAd8Run = 24;  // tiles of a warp in a long run of CTAs
 template <int kKind, class Table>
@@ -893,34 +902,42 @@ struct NormAt {
   bool fast;  // contiguous and aligned
 };
 
-// tile of 1,024 entries: four loads of eight a lane under way at once
+// a lane's part of a tile, its first entry e0: four loads of eight under way at once (with eight 774M bf16 entries took
+// 291 us instead of 257)
 template <class E>
-__device__ __forceinline__ double tile_sumsq(const NormAt& A, const NormTensor& T, int tile, int lane) {
+__device__ __forceinline__ double run_sumsq(const NormAt& A, const NormTensor& T, int64_t e0) {
+  constexpr int kLoads = kNormTile / kAdBlock;
   const E* const p = reinterpret_cast<const E*>(A.g);
-  const int64_t e0 = (int64_t)tile * kNormTile + lane * 8;
   double d = 0.0;
-  if (A.fast && (int64_t)(tile + 1) * kNormTile <= A.n) {
-    Raw8<E> x[4];
+  if (A.fast) {
+    Raw8<E> x[kLoads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k].load(p + e0 + k * kAdBlock);
+    for (int k = 0; k < kLoads; ++k) {
+      x[k] = Raw8<E>{};
+      if (e0 + k * kAdBlock + 8 <= A.n) x[k].load(p + e0 + k * kAdBlock);
+    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) d += sumsq(x[k]);
-  } else {
+    for (int k = 0; k < kLoads; ++k) d += sumsq(x[k]);
+    const int64_t tail = A.n & ~(int64_t)7;  // the last entries, short of eight: one lane's
+    if (tail < A.n && tail >= e0 && tail < e0 + kLoads * kAdBlock && (tail - e0) % kAdBlock == 0) {
+      for (int64_t e = tail; e < A.n; ++e) d = fma((double)to_f32(p[e]), (double)to_f32(p[e]), d);
+    }
+    return d;
+  }
+  const bool stride = T.ld != T.cols;
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      const int64_t e = e0 + k * kAdBlock;
-      if (e >= A.n) break;
-      const bool stride = T.ld != T.cols;
-      if (T.vec && e + 8 <= A.n) {
-        Raw8<E> x;
-        x.load(p + (stride ? strided(e, T.cols, T.ld) : e));
-        d += sumsq(x);
-      } else {
-        float g[8];
+  for (int k = 0; k < kLoads; ++k) {
+    const int64_t e = e0 + k * kAdBlock;
+    if (e >= A.n) break;
+    if (T.vec && e + 8 <= A.n) {
+      Raw8<E> x;
+      x.load(p + (stride ? strided(e, T.cols, T.ld) : e));
+      d += sumsq(x);
+    } else {
+      float g[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = e + j < A.n ? to_f32(p[stride ? strided(e + j, T.cols, T.ld) : e + j]) : 0.f;
-        d += sumsq_f64(g);
-      }
+      for (int j = 0; j < 8; ++j) g[j] = e + j < A.n ? to_f32(p[stride ? strided(e + j, T.cols, T.ld) : e + j]) : 0.f;
+      d += sumsq_f64(g);
     }
   }
   return d;
@@ -947,7 +964,9 @@ __global__ void __launch_bounds__(256, 4) k_grad_norm(const __grid_constant__ No
   follow_previous();
   NormAt A{};
   bool bf16 = false;
-  for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < a.total_tiles; b += gridDim.x * 8) {
+  // a stretch of its own for each CTA: 774M bf16 entries 268 us, dealt out in turn 284
+  const int stop = (int)((int64_t)a.total_tiles * (blockIdx.x + 1) / gridDim.x);
+  for (int b = (int)((int64_t)a.total_tiles * blockIdx.x / gridDim.x) + (threadIdx.x >> 5); b < stop; b += 8) {
     if (b >= end) {
       li = tensor_of_warp(a.t, a.n_tensors, b, li);
       const NormTensor& T = a.t[li];
@@ -955,7 +974,8 @@ __global__ void __launch_bounds__(256, 4) k_grad_norm(const __grid_constant__ No
       bf16 = T.bf16;
       end = li + 1 < a.n_tensors ? a.t[li + 1].tile_begin : a.total_tiles;
     }
-    acc += bf16 ? tile_sumsq<__nv_bfloat16>(A, a.t[li], b - A.begin, lane) : tile_sumsq<float>(A, a.t[li], b - A.begin, lane);
+    const int64_t e0 = (int64_t)(b - A.begin) * kNormTile + lane * 8;
+    acc += bf16 ? run_sumsq<__nv_bfloat16>(A, a.t[li], e0) : run_sumsq<float>(A, a.t[li], e0);
   }
   const double mine = cta_sum(acc);
   __shared__ bool last;
@@ -990,8 +1010,8 @@ cudaError_t launch_grad_norm(const NormArgs& a, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- conversion
-// A warp takes a tile of two blocks: the loads of both are under way before either is converted. One tile a warp, as in
-// k_adamw32 (65.6M entries to 32 bits: 102 us; with a grid of resident CTAs 118 us).
+// Reads 8 and writes 2 bytes an entry, or the other way round; one block a warp, as in k_adamw32 (65.6M entries to 32
+// bits: 99 us; with a grid of resident CTAs 118 us).
 namespace {
 __device__ __forceinline__ void convert_to8(const ConvTensor& T, int64_t blk, int lane, const float (&m)[8], float (&r)[8]) {
   const int64_t e0 = blk * kAdBlock + lane * 8;
@@ -1016,42 +1036,33 @@ __device__ __forceinline__ void convert_to32(const ConvTensor& T, int64_t blk, i
 }
 }  // namespace
 
-__global__ void __launch_bounds__(256) k_adamw_convert(const __grid_constant__ ConvTable tb) {
+constexpr int kConvWarps = 8;
+__global__ void __launch_bounds__(32 * kConvWarps) k_adamw_convert(const __grid_constant__ ConvTable tb) {
   follow_previous();
   const int lane = threadIdx.x & 31;
-  int li = 0, end = 0;
-  for (int b = blockIdx.x * 8 + (threadIdx.x >> 5); b < tb.total_tiles; b += gridDim.x * 8) {
-    if (b >= end) {
-      li = tensor_of(tb, b, li);
-      end = li + 1 < tb.n_tensors ? tb.t[li + 1].tile_begin : tb.total_tiles;
-    }
-    const ConvTensor& T = tb.t[li];
-    const int64_t n = T.n, blk = 2 * (int64_t)(b - T.tile_begin), e0 = blk * kAdBlock + lane * 8;
-    const bool two_blocks = (blk + 1) * kAdBlock < n;
-    const bool v0 = T.vec && e0 + 8 <= n, v1 = T.vec && e0 + kAdBlock + 8 <= n;
-    if (tb.to8) {
-      float m0[8], r0[8], m1[8], r1[8];
-      load(reinterpret_cast<const float*>(T.m32), e0, n, e0, v0, m0);
-      load(reinterpret_cast<const float*>(T.v32), e0, n, e0, v0, r0);
-      load(reinterpret_cast<const float*>(T.m32), e0 + kAdBlock, n, e0 + kAdBlock, v1, m1);
-      load(reinterpret_cast<const float*>(T.v32), e0 + kAdBlock, n, e0 + kAdBlock, v1, r1);
-      convert_to8(T, blk, lane, m0, r0);
-      if (two_blocks) convert_to8(T, blk + 1, lane, m1, r1);
-    } else {
-      const uint16_t* const sc = reinterpret_cast<const uint16_t*>(T.scales);
-      const uint8_t *pm = reinterpret_cast<const uint8_t*>(T.m8), *pr = reinterpret_cast<const uint8_t*>(T.v8);
-      const uint32_t s0 = sc[blk], s1 = two_blocks ? sc[blk + 1] : 0u;
-      const uint2 m0 = load_codes(pm, e0, n, v0), r0 = load_codes(pr, e0, n, v0);
-      const uint2 m1 = load_codes(pm, e0 + kAdBlock, n, v1), r1 = load_codes(pr, e0 + kAdBlock, n, v1);
-      convert_to32(T, blk, lane, s0, m0, r0);
-      if (two_blocks) convert_to32(T, blk + 1, lane, s1, m1, r1);
-    }
+  const unsigned unit = blockIdx.x * kConvWarps + (threadIdx.x >> 5);  // block of the launch, two for each tile
+  const int tile = (int)(unit >> 1);
+  if (tile >= tb.total_tiles) return;
+  const ConvTensor& T = tb.t[tensor_of(tb, tile, 0)];
+  const int64_t n = T.n, blk = 2 * (int64_t)(tile - T.tile_begin) + (unit & 1), e0 = blk * kAdBlock + lane * 8;
+  if (blk * kAdBlock >= n) return;
+  const bool vec = T.vec && e0 + 8 <= n;
+  if (tb.to8) {
+    float m[8], r[8];
+    load(reinterpret_cast<const float*>(T.m32), e0, n, e0, vec, m);
+    load(reinterpret_cast<const float*>(T.v32), e0, n, e0, vec, r);
+    convert_to8(T, blk, lane, m, r);
+  } else {
+    const uint32_t sc = reinterpret_cast<const uint16_t*>(T.scales)[blk];
+    const uint2 cm = load_codes(reinterpret_cast<const uint8_t*>(T.m8), e0, n, vec);
+    const uint2 cr = load_codes(reinterpret_cast<const uint8_t*>(T.v8), e0, n, vec);
+    convert_to32(T, blk, lane, sc, cm, cr);
   }
 }
 
 cudaError_t launch_adamw_convert(const ConvTable& tb, cudaStream_t s) {
-  const int want = (tb.total_tiles + 7) / 8;
-  return launch(k_adamw_convert, want < 1 ? 1 : want, 256, 0, s, tb);
+  const int want = (int)((2 * (int64_t)tb.total_tiles + kConvWarps - 1) / kConvWarps);
+  return launch(k_adamw_convert, want < 1 ? 1 : want, 32 * kConvWarps, 0, s, tb);
 }
 
 }  // namespace smuon
