@@ -1491,9 +1491,9 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
     T.lr_scale = ls; T.wd = wd; T.id = (uint32_t)i;
     T.flags = (has_stride(W) ? kAdWStride : 0) | (has_stride(G[i]) ? kAdGStride : 0);
     const int lane = eight ? 16 : 8;
-    if (vec_of(W, lane) && vec_of(G[i], lane) && vec_of(st->m[i], lane) && vec_of(st->v[i], lane) &&
-        (!master || vec_of(st->master[i], lane)))
-      T.flags |= kAdVec;
+    if (vec_of(st->m[i], lane) && vec_of(st->v[i], lane) && (!master || vec_of(st->master[i], lane))) T.flags |= kAdVecState;
+    if (vec_of(W, lane)) T.flags |= kAdVecW;
+    if (vec_of(G[i], lane)) T.flags |= kAdVecG;
     const int kind = (master ? AD_W_MASTER : W.dtype == SMUON_BF16 ? AD_W_BF16 : AD_W_F32) |
                      (G[i].dtype == SMUON_BF16 ? AD_G_BF16 : 0) | (eight ? AD_8BIT : 0);
     by_kind[kind].push_back(T);
@@ -1607,9 +1607,9 @@ smuon_status check_norm_tensors(const smuon_mat* G, int32_t n) {
   return SMUON_OK;
 }
 
-// ws of a norm: the arrival count, the table, one partial sum per CTA
+// ws of a norm: the arrival count, the table (a tensor off its vector addresses takes two places), one sum per CTA
 constexpr size_t kNormHead = 256;
-size_t norm_table_bytes(int32_t n) { return (size_t)round_up((int64_t)n * (int64_t)sizeof(NormTensor), 256); }
+size_t norm_table_bytes(int32_t n) { return (size_t)round_up(2 * (int64_t)n * (int64_t)sizeof(NormTensor), 256); }
 size_t norm_ws_bytes(int32_t n) { return kNormHead + norm_table_bytes(n) + (size_t)round_up(8 * kNormMaxGrid, 256); }
 
 smuon_status prepare_norm(const smuon_mat* G, int32_t n, double max_norm, float* d_out, int32_t* d_skip, void* ws,
@@ -1625,18 +1625,35 @@ smuon_status prepare_norm(const smuon_mat* G, int32_t n, double max_norm, float*
   NormTensor* const t = reinterpret_cast<NormTensor*>(bytes.data() + kNormHead);
   int32_t used = 0;
   int64_t tiles = 0;
-  for (int i = 0; i < n; ++i) {
-    const int64_t e = entries(G[i]);
-    if (!e) continue;
+  auto add = [&](const smuon_mat& g) {
+    const int64_t e = entries(g);
+    if (!e) return;
     NormTensor& T = t[used++];
-    T.g = G[i].data; T.n = e; T.cols = G[i].cols;
-    T.ld = has_stride(G[i]) ? G[i].ld : G[i].cols;
+    T.g = g.data; T.n = e; T.cols = g.cols;
+    T.ld = has_stride(g) ? g.ld : g.cols;
     T.tile_begin = (int32_t)tiles;
-    T.bf16 = G[i].dtype == SMUON_BF16;
-    T.vec = vec_of(G[i], 8);
+    T.bf16 = g.dtype == SMUON_BF16;
+    T.vec = vec_of(g, 8);
     tiles += (e + kNormTile - 1) / kNormTile;
+    ex->bytes += (double)e * dtype_size(g.dtype);
+  };
+  for (int i = 0; i < n; ++i) {
+    const int es = dtype_size(G[i].dtype);
+    const int64_t e = entries(G[i]);
+    const int64_t head = (8 - (int64_t)(reinterpret_cast<uintptr_t>(G[i].data) / es % 8)) % 8;
+    if (head && e > head && !has_stride(G[i]) && e < ((int64_t)1 << 31)) {  // up to seven entries, then vectors
+      smuon_mat first = G[i], rest = G[i];
+      first.rows = rest.rows = 1;
+      first.cols = first.ld = (int32_t)head;
+      rest.data = reinterpret_cast<char*>(G[i].data) + head * es;
+      rest.cols = (int32_t)(e - head);
+      rest.ld = rest.cols;
+      add(first);
+      add(rest);
+    } else {
+      add(G[i]);
+    }
     if (tiles > ((int64_t)1 << 30)) return fail(SMUON_ERR_UNSUPPORTED, "more than 2^40 entries in all");
-    ex->bytes += (double)e * dtype_size(G[i].dtype);
   }
   DevInfo di;
   if ((s = device_info(&di)) != SMUON_OK) return s;

@@ -26,9 +26,9 @@ struct AdTensor {
   uint32_t id;            // index in the call's lists: key word 1 of its rounding stream
   int32_t flags;          // kAd*
 };
-constexpr int32_t kAdVec = 1;      // a lane's entries (eight, with 8-bit moments sixteen) are aligned vectors in each operand
-constexpr int32_t kAdWStride = 2;  // W has a row stride
-constexpr int32_t kAdGStride = 4;
+// a lane's entries (eight, with 8-bit moments sixteen) are aligned vectors in the moments and the master, in W, in G
+constexpr int32_t kAdVecState = 1, kAdVecW = 2, kAdVecG = 4, kAdVec = 7;
+constexpr int32_t kAdWStride = 8, kAdGStride = 16;  // W, G has a row stride
 
 // What changes from call to call, beside the table (which a plan keeps).
 struct AdHyper {

@@ -101,6 +101,31 @@ __device__ __forceinline__ int64_t strided(int64_t e, int32_t cols, int64_t ld) 
   return r * ld + (e - r * cols);
 }
 
+// element offsets of entries e, e + 32, e + 64, ... (cols 0: no row stride)
+struct Places {
+  int64_t at, ld;
+  int32_t col, cols;
+  __device__ __forceinline__ Places(int64_t e, int32_t cols_, int64_t ld_) : at(e), ld(ld_), col(0), cols(cols_) {
+    if (cols) {
+      const int64_t r = e / cols;
+      col = (int32_t)(e - r * cols);
+      at = r * ld + col;
+    }
+  }
+  __device__ __forceinline__ int64_t take() {
+    const int64_t here = at;
+    at += 32;
+    if (cols) {
+      col += 32;
+      while (col >= cols) {
+        col -= cols;
+        at += ld - cols;
+      }
+    }
+    return here;
+  }
+};
+
 // eight entries from entry e0 on, which lies at element `at` (all eight in one row, where there are eight)
 template <class T>
 __device__ __forceinline__ void load(const T* p, int64_t e0, int64_t n, int64_t at, bool vec, float (&x)[8]) {
@@ -284,19 +309,63 @@ __device__ __forceinline__ float sqrt_approx(float v) {
   return r;
 }
 
-// A block of any alignment or stride, entry by entry; with 8-bit moments also one whose scales leave the range of the fast
-// form or whose values are not finite. With float32 moments the lanes' entries lie side by side, so the accesses coalesce.
+// A block of any alignment or stride, float32 moments: the lanes' entries lie side by side, so the accesses coalesce.
 template <int kKind>
-__device__ __noinline__ void step_block_any(const AdTensor& T, int64_t blk, int lane, const Consts& c) {
+__device__ __noinline__ void step_block32(const AdTensor& T, int64_t blk, int lane, const Consts& c) {
   using K = Kind<kKind>;
   using WT = typename K::W;
   using GT = typename K::G;
-  const int64_t n = T.n;
+  const float lr = c.lr * T.lr_scale, step = lr * c.ic1, decay = lr * T.wd;
+  const int64_t first = blk * kAdBlock + lane;
+  const int left = (int)min(T.n - first, (int64_t)kAdBlock);
+  float* const pm = reinterpret_cast<float*>(T.m) + first;
+  float* const pv = reinterpret_cast<float*>(T.v) + first;
+  Places wp(first, T.flags & kAdWStride ? T.cols : 0, T.w_ld), gp(first, T.flags & kAdGStride ? T.cols : 0, T.g_ld);
+#pragma unroll 1
+  for (int k0 = 0; k0 < 8; k0 += 4) {  // four entries' loads before the first use
+    float w[4], g[4], m[4], v[4];
+    WT* to[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = 32 * (k0 + j);
+      to[j] = reinterpret_cast<WT*>(T.w) + wp.take();
+      const GT* const from = reinterpret_cast<const GT*>(T.g) + gp.take();
+      w[j] = g[j] = m[j] = v[j] = 0.f;
+      if (d < left) {
+        g[j] = to_f32(*from);
+        w[j] = K::master ? T.master[first + d] : to_f32(*to[j]);
+        m[j] = pm[d];
+        v[j] = pv[d];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = 32 * (k0 + j);
+      if (d < left) {
+        const float x = __fmul_rn(c.gs, g[j]);
+        m[j] = __fadd_rn(__fmul_rn(c.b1, m[j]), __fmul_rn(c.c1, x));
+        v[j] = __fadd_rn(__fmul_rn(c.b2, v[j]), __fmul_rn(c.c2, __fmul_rn(x, x)));
+        w[j] = weight_step(w[j], m[j], __fsqrt_rn(v[j]), decay, step, c);
+        if (K::master) T.master[first + d] = w[j];
+        put(to[j], w[j]);
+        pm[d] = m[j];
+        pv[d] = v[j];
+      }
+    }
+  }
+}
+
+// A block with 8-bit moments of any alignment, or whose scales leave the range of the fast form, or whose values are not
+// finite: entry by entry.
+template <int kKind>
+__device__ __noinline__ void step_block8(const AdTensor& T, int64_t blk, int lane, const Consts& c) {
+  using K = Kind<kKind>;
+  using WT = typename K::W;
+  using GT = typename K::G;
+  const int64_t n = T.n, first = blk * kAdBlock + lane * 8;
   const bool ws = T.flags & kAdWStride, gst = T.flags & kAdGStride;
   const float lr = c.lr * T.lr_scale, step = lr * c.ic1, decay = lr * T.wd;
-  const uint32_t sc = K::eight ? *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk) : 0u;
-  const int64_t first = blk * kAdBlock + (K::eight ? lane * 8 : lane);
-  constexpr int per = K::eight ? 1 : 32;
+  const uint32_t sc = *reinterpret_cast<const uint16_t*>(T.scales + 2 * blk);
   float m[8], r[8];
 #pragma unroll
   for (int k0 = 0; k0 < 8; k0 += 4) {  // four entries' loads before the first use
@@ -304,55 +373,39 @@ __device__ __noinline__ void step_block_any(const AdTensor& T, int64_t blk, int 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + j;
-      const int64_t e = first + k * per;
+      const int64_t e = first + k;
       w[j] = g[j] = m[k] = r[k] = 0.f;
       if (e < n) {
         g[j] = to_f32(reinterpret_cast<const GT*>(T.g)[gst ? strided(e, T.cols, T.g_ld) : e]);
         w[j] = K::master ? T.master[e] : to_f32(reinterpret_cast<const WT*>(T.w)[ws ? strided(e, T.cols, T.w_ld) : e]);
-        if (K::eight) {
-          m[k] = decode1(reinterpret_cast<const uint8_t*>(T.m)[e]);
-          r[k] = decode1(reinterpret_cast<const uint8_t*>(T.v)[e]);
-        } else {
-          m[k] = reinterpret_cast<const float*>(T.m)[e];
-          r[k] = reinterpret_cast<const float*>(T.v)[e];
-        }
+        m[k] = decode1(reinterpret_cast<const uint8_t*>(T.m)[e]);
+        r[k] = decode1(reinterpret_cast<const uint8_t*>(T.v)[e]);
       }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + j;
-      const int64_t e = first + k * per;
-      if (K::eight) {
-        m[k] = __fmul_rn(m[k], scale_of(sc & 255u));
-        r[k] = __fmul_rn(r[k], scale_of(sc >> 8));
-        r[k] = __fmul_rn(r[k], r[k]);
-      }
+      const int64_t e = first + k;
+      m[k] = __fmul_rn(m[k], scale_of(sc & 255u));
+      r[k] = __fmul_rn(r[k], scale_of(sc >> 8));
       const float x = __fmul_rn(c.gs, g[j]);
       m[k] = __fadd_rn(__fmul_rn(c.b1, m[k]), __fmul_rn(c.c1, x));
-      const float v = __fadd_rn(__fmul_rn(c.b2, r[k]), __fmul_rn(c.c2, __fmul_rn(x, x)));
-      r[k] = __fsqrt_rn(v);
+      r[k] = __fsqrt_rn(__fadd_rn(__fmul_rn(c.b2, __fmul_rn(r[k], r[k])), __fmul_rn(c.c2, __fmul_rn(x, x))));
       if (e < n) {
         w[j] = weight_step(w[j], m[k], r[k], decay, step, c);
         if (K::master) T.master[e] = w[j];
         put(reinterpret_cast<WT*>(T.w) + (ws ? strided(e, T.cols, T.w_ld) : e), w[j]);
-        if (!K::eight) {
-          reinterpret_cast<float*>(T.m)[e] = m[k];
-          reinterpret_cast<float*>(T.v)[e] = v;
-        }
       } else {
         m[k] = r[k] = 0.f;  // past a short last block
       }
     }
   }
-  if (K::eight) {
-    const int64_t e0 = blk * kAdBlock + lane * 8;
-    const uint32_t bm = block_exponent(m), br = block_exponent(r);
-    const uint64_t grp = (uint64_t)e0 >> 3;
-    const uint4 rnd = crng::philox4x32_10(make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), c.t, 1u), c.seed, T.id);
-    store_codes(reinterpret_cast<uint8_t*>(T.m), e0, n, false, encode8<true>(m, bm, rnd));
-    store_codes(reinterpret_cast<uint8_t*>(T.v), e0, n, false, encode8<true>(r, br, rnd));
-    if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
-  }
+  const uint32_t bm = block_exponent(m), br = block_exponent(r);
+  const uint64_t grp = (uint64_t)first >> 3;
+  const uint4 rnd = crng::philox4x32_10(make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), c.t, 1u), c.seed, T.id);
+  store_codes(reinterpret_cast<uint8_t*>(T.m), first, n, false, encode8<true>(m, bm, rnd));
+  store_codes(reinterpret_cast<uint8_t*>(T.v), first, n, false, encode8<true>(r, br, rnd));
+  if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
 }
 
 // Eight entries of a lane, float32 moments, vector operands.
@@ -525,13 +578,32 @@ __device__ __noinline__ void copy_rows(uint32_t dst, const E* base, int64_t e0, 
   }
 }
 
+// the same for an operand off its vector addresses, entry by entry
+template <class E>
+__device__ __noinline__ void copy_entries(E* dst, const E* base, int64_t e0, int64_t n, int lane, int32_t cols, int64_t ld) {
+  const int left = (int)min(n - e0, (int64_t)kAdTile);
+  Places p(e0 + lane, cols, ld);
+#pragma unroll 1
+  for (int k0 = lane; k0 < kAdTile; k0 += 8 * 32) {
+    E x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t at = p.take();
+      x[j] = k0 + 32 * j < left ? base[at] : E(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dst[k0 + 32 * j] = x[j];
+  }
+}
+
 // starts the copies of a tile; returns the exponent bytes of the lane's block
 template <int kKind>
-__device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int lane, uint32_t stage) {
+__device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int lane, char* stage_ptr) {
   using L = Stage<kKind>;
   using K = Kind<kKind>;
   using ST = typename L::ST;
   using GT = typename K::G;
+  const uint32_t stage = (uint32_t)__cvta_generic_to_shared(stage_ptr);
   const void* const w = K::master ? T.master : T.w;
   if ((int64_t)(tile + 1) * kAdTile <= T.n && (T.flags & (kAdVec | kAdWStride | kAdGStride)) == kAdVec) {
     const uint32_t lane16 = lane * 16;
@@ -541,17 +613,22 @@ __device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int
     copy_operand<ST>(stage + L::w, w, tile, lane16);
     return reinterpret_cast<const uint16_t*>(T.scales)[2 * (int64_t)tile + (lane >> 4)];
   }
-  if (!(T.flags & kAdVec)) return 0;
+  if (!(T.flags & kAdVecState)) return 0;
   const int64_t e0 = (int64_t)tile * kAdTile, n = T.n, blk = 2 * (int64_t)tile + (lane >> 4);
-  copy_rows(stage + L::g, reinterpret_cast<const GT*>(T.g), e0, n, lane, T.flags & kAdGStride ? T.cols : 0, T.g_ld);
-  copy_rows(stage + L::w, reinterpret_cast<const ST*>(w), e0, n, lane, !K::master && (T.flags & kAdWStride) ? T.cols : 0, T.w_ld);
+  const GT* const g = reinterpret_cast<const GT*>(T.g);
+  const int32_t g_cols = T.flags & kAdGStride ? T.cols : 0, w_cols = !K::master && (T.flags & kAdWStride) ? T.cols : 0;
+  if (T.flags & kAdVecG) copy_rows(stage + L::g, g, e0, n, lane, g_cols, T.g_ld);
+  else copy_entries(reinterpret_cast<GT*>(stage_ptr + L::g), g, e0, n, lane, g_cols, T.g_ld);
+  const ST* const ws = reinterpret_cast<const ST*>(w);
+  if (K::master || (T.flags & kAdVecW)) copy_rows(stage + L::w, ws, e0, n, lane, w_cols, T.w_ld);
+  else copy_entries(reinterpret_cast<ST*>(stage_ptr + L::w), ws, e0, n, lane, w_cols, T.w_ld);
   copy_rows(stage + L::m, reinterpret_cast<const uint8_t*>(T.m), e0, n, lane, 0, 0);
   copy_rows(stage + L::v, reinterpret_cast<const uint8_t*>(T.v), e0, n, lane, 0, 0);
   return blk * kAdBlock < n ? reinterpret_cast<const uint16_t*>(T.scales)[blk] : 0u;
 }
 
-// A tile with vector operands, 8-bit moments, a block to each half of the warp (sixteen entries a lane: what a block
-// costs beside its entries is then paid once for two): the same values as step_block_any with fewer instructions (370 a warp
+// A tile with vector moments, 8-bit, a block to each half of the warp (sixteen entries a lane: what a block
+// costs beside its entries is then paid once for two): the same values as step_block8 with fewer instructions (370 a warp
 // for 256 entries, the first form took 770), which are what bounds it.
 //  - b1 m = (b1 2^k) code and b2 v = (b2 2^2k) code^2: a power of two commutes with the rounding, so the factor is
 //    formed once a block (while it is a normal number).
@@ -562,7 +639,7 @@ __device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int
 // false where a value leaves the range in which this holds (nothing is written then).
 template <int kKind>
 __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane, const Consts& c, const AdHyper& h,
-                                           const char* stage, uint32_t sc) {
+                                           char* stage, uint32_t sc) {
   using K = Kind<kKind>;
   using L = Stage<kKind>;
   using WT = typename K::W;
@@ -638,23 +715,44 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
       orr[(k >> 2) + 1] = x.y;
     }
   }
+  if (!(T.flags & kAdVecW)) {  // W off its vector addresses: through the stage, entry by entry
+    __syncwarp();  // its own copy has been read
+    WT* const out = reinterpret_cast<WT*>(stage + L::w);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      float x, y;
+      split(w.pair(k), x, y);
+      put(out + at + k, x);
+      put(out + at + k + 1, y);
+    }
+    __syncwarp();
+    const int64_t t0 = (int64_t)tile * kAdTile;
+    Places p(t0 + lane, T.flags & kAdWStride ? T.cols : 0, T.w_ld);
+    for (int k = lane; k < kAdTile; k += 32) {
+      const int64_t to = p.take();
+      if (t0 + k < T.n) reinterpret_cast<WT*>(T.w)[to] = out[k];
+    }
+  }
   if (e0 >= T.n) return true;
   if ((lane & 15) == 0) reinterpret_cast<uint16_t*>(T.scales)[2 * (int64_t)tile + upper] = (uint16_t)(bm | br << 8);
+  const bool vw = T.flags & kAdVecW;
   WT* const pw = reinterpret_cast<WT*>(T.w) + (T.flags & kAdWStride ? strided(e0, T.cols, T.w_ld) : e0);
   uint8_t *const pm = reinterpret_cast<uint8_t*>(T.m) + e0, *const pr = reinterpret_cast<uint8_t*>(T.v) + e0;
   if (e0 + 16 <= T.n) {
-    if constexpr (K::master) {
-      w.store(T.master + e0);
-      Raw16<WT> b;
+    if constexpr (K::master) w.store(T.master + e0);
+    if (vw) {
+      if constexpr (K::master) {
+        Raw16<WT> b;
 #pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        float x, y;
-        split(w.pair(k), x, y);
-        b.put(k, x, y);
+        for (int k = 0; k < 16; k += 2) {
+          float x, y;
+          split(w.pair(k), x, y);
+          b.put(k, x, y);
+        }
+        b.store(pw);
+      } else {
+        w.store(pw);
       }
-      b.store(pw);
-    } else {
-      w.store(pw);
     }
     *reinterpret_cast<uint4*>(pm) = make_uint4(om[0], om[1], om[2], om[3]);
     *reinterpret_cast<uint4*>(pr) = make_uint4(orr[0], orr[1], orr[2], orr[3]);
@@ -668,7 +766,7 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
       for (int j = 0; j < 2; ++j)
         if (k + j < left) {
           if constexpr (K::master) T.master[e0 + k + j] = x[j];
-          put(pw + k + j, x[j]);
+          if (vw) put(pw + k + j, x[j]);
           pm[k + j] = (uint8_t)(om[k >> 2] >> (8 * ((k + j) & 3)));
           pr[k + j] = (uint8_t)(orr[k >> 2] >> (8 * ((k + j) & 3)));
         }
@@ -722,10 +820,10 @@ __global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_con
     const AdTensor& T = tensor_at(tb, at.li, mine, at.which);
     const int64_t blk = 2 * (int64_t)(at.b - T.tile_begin) + (unit & 1);
     if (skip) {  // nothing
-    } else if ((T.flags & kAdVec) && (blk + 1) * kAdBlock <= T.n) {
+    } else if ((T.flags & kAdVec) == kAdVec && (blk + 1) * kAdBlock <= T.n) {
       step_lane32<kKind>(T, blk * kAdBlock + lane * 8, c);
     } else if (blk * kAdBlock < T.n) {
-      step_block_any<kKind>(T, blk, lane, c);
+      step_block32<kKind>(T, blk, lane, c);
     }
   }
   advance(h, skip);
@@ -749,7 +847,6 @@ __global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __gri
   const Consts c = consts_of(h);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   char* const ring = smem + warp * 2 * L::bytes;
-  const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
   AdTensor* const mine = slots[warp];
   const int first = (int)((int64_t)tb.total_tiles * blockIdx.x / gridDim.x);
   Walk<Table> next(first + warp, (int)((int64_t)tb.total_tiles * (blockIdx.x + 1) / gridDim.x));
@@ -757,7 +854,7 @@ __global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __gri
   uint32_t sc_next = 0;
   if (more) {
     const AdTensor& N = tensor_at(tb, next.li, mine, next.which);
-    sc_next = fetch_tile8<kKind>(N, next.b - N.tile_begin, lane, ring_addr);
+    sc_next = fetch_tile8<kKind>(N, next.b - N.tile_begin, lane, ring);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
   if (skip) {
@@ -773,12 +870,12 @@ __global__ void __launch_bounds__(32 * kAd8Warps, kAd8Ctas) k_adamw8(const __gri
     __syncwarp();  // every lane has read the stage that is filled now
     if (more) {
       const AdTensor& N = tensor_at(tb, next.li, mine, next.which);
-      sc_next = fetch_tile8<kKind>(N, next.b - N.tile_begin, lane, ring_addr + (turn ^ 1) * L::bytes);
+      sc_next = fetch_tile8<kKind>(N, next.b - N.tile_begin, lane, ring + (turn ^ 1) * L::bytes);
     }
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
     __syncwarp();
-    if ((T.flags & kAdVec) && step_tile8<kKind>(T, tile, lane, c, h, ring + turn * L::bytes, sc)) continue;
-    for (int k = 0; k < 2 && (2 * (int64_t)tile + k) * kAdBlock < T.n; ++k) step_block_any<kKind>(T, 2 * (int64_t)tile + k, lane, c);
+    if ((T.flags & kAdVecState) && step_tile8<kKind>(T, tile, lane, c, h, ring + turn * L::bytes, sc)) continue;
+    for (int k = 0; k < 2 && (2 * (int64_t)tile + k) * kAdBlock < T.n; ++k) step_block8<kKind>(T, 2 * (int64_t)tile + k, lane, c);
   }
   advance(h, skip);
 }
@@ -905,7 +1002,7 @@ struct NormAt {
 // a lane's part of a tile, its first entry e0: four loads of eight under way at once (with eight 774M bf16 entries took
 // 291 us instead of 257)
 template <class E>
-__device__ __forceinline__ double run_sumsq(const NormAt& A, const NormTensor& T, int64_t e0) {
+__device__ __forceinline__ double run_sumsq(const NormAt& A, const NormTensor& T, int64_t e0, int lane) {
   constexpr int kLoads = kNormTile / kAdBlock;
   const E* const p = reinterpret_cast<const E*>(A.g);
   double d = 0.0;
@@ -925,20 +1022,31 @@ __device__ __forceinline__ double run_sumsq(const NormAt& A, const NormTensor& T
     return d;
   }
   const bool stride = T.ld != T.cols;
+  if (T.vec) {  // a row stride, eight in one row
+#pragma unroll 1
+    for (int k = 0; k < kLoads; ++k) {
+      const int64_t e = e0 + k * kAdBlock;
+      if (e + 8 > A.n) break;
+      Raw8<E> x;
+      x.load(p + strided(e, T.cols, T.ld));
+      d += sumsq(x);
+    }
+    return d;
+  }
+  // off the vector addresses: entries 32 apart, which the lanes' accesses cover side by side
+  const int64_t first = e0 - lane * 7;
+  Places at(first, stride ? T.cols : 0, T.ld);
 #pragma unroll 1
   for (int k = 0; k < kLoads; ++k) {
-    const int64_t e = e0 + k * kAdBlock;
-    if (e >= A.n) break;
-    if (T.vec && e + 8 <= A.n) {
-      Raw8<E> x;
-      x.load(p + (stride ? strided(e, T.cols, T.ld) : e));
-      d += sumsq(x);
-    } else {
-      float g[8];
+    float g[8], s = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = e + j < A.n ? to_f32(p[stride ? strided(e + j, T.cols, T.ld) : e + j]) : 0.f;
-      d += sumsq_f64(g);
+    for (int j = 0; j < 8; ++j) {
+      const int64_t to = at.take();
+      g[j] = first + 256 * k + 32 * j < A.n ? to_f32(p[to]) : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(g[j], g[j], s);
+    d += s >= kNormLow && s <= kNormHigh ? (double)s : sumsq_f64(g);
   }
   return d;
 }
@@ -975,7 +1083,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_norm(const __grid_constant__ No
       end = li + 1 < a.n_tensors ? a.t[li + 1].tile_begin : a.total_tiles;
     }
     const int64_t e0 = (int64_t)(b - A.begin) * kNormTile + lane * 8;
-    acc += bf16 ? run_sumsq<__nv_bfloat16>(A, a.t[li], e0) : run_sumsq<float>(A, a.t[li], e0);
+    acc += bf16 ? run_sumsq<__nv_bfloat16>(A, a.t[li], e0, lane) : run_sumsq<float>(A, a.t[li], e0, lane);
   }
   const double mine = cta_sum(acc);
   __shared__ bool last;

@@ -228,6 +228,54 @@ def test_column_ranges_and_odd_addresses(eight, wdt, gdt):
         assert torch.all(sbuf[0] == 77) and torch.all(sbuf[-1] == 77)
 
 
+@pytest.mark.parametrize("master", [False, True])
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("w_off,g_off", [(1, 0), (0, 1), (3, 5)])
+def test_long_tensors_off_their_vector_addresses(w_off, g_off, eight, master):
+    """Several tiles each: a flat tensor, rows of odd length, rows of a whole number of vectors at an odd offset, a single
+    column; W, G or both off the addresses that vectors need. Entries beside the tensors stay as they were."""
+    rng = np.random.default_rng(17)
+    wdt, gdt = (BF16, F32) if master else (F32, BF16)
+    W, G, refs, gs, bufs = [], [], [], [], []
+    for i, (r, c, ld) in enumerate([(1, 5003, 5010), (37, 133, 140), (61, 64, 80), (1500, 1, 6), (3, 1100, 1104)]):
+        w, g, _, _ = draw_tensor(rng, (r, c))
+        wb = torch.full((r, ld + 3), 7.0, dtype=wdt, device="cuda")
+        gb = torch.full((r, ld + 5), 9.0, dtype=gdt, device="cuda")
+        W.append(wb[:, w_off:w_off + c])
+        G.append(gb[:, g_off:g_off + c])
+        W[i].copy_(torch.from_numpy(w.astype(np.float32)).reshape(r, c))
+        G[i].copy_(torch.from_numpy(g.astype(np.float32)).reshape(r, c))
+        bufs.append((wb, c))
+        refs.append(Reference(f64(W[i].contiguous()), np.zeros(r * c), np.zeros(r * c), eight, i, 4, bf16=master, master=master))
+        gs.append(f64(G[i].contiguous()))
+    opt = S.AdamW(W, bits=8 if eight else 32, master=master, weight_decay=WD, seed=4)
+    plan = S.AdamWPlan(opt, G, B1, B2, EPS)
+    for t in (1, 2):
+        plan.run(LR)
+        step_refs(opt, refs, gs, t)
+    for (wb, c) in bufs:
+        assert torch.all(wb[:, :w_off] == 7.0) and torch.all(wb[:, w_off + c:] == 7.0)
+
+
+@pytest.mark.parametrize("eps", [1e-8, 1e-15, 1e-30])
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.0, 0.999), (0.9, 0.0)])
+@pytest.mark.parametrize("size", [1e-3, 1e-17, 1e-19])
+def test_small_eps_and_small_gradients(size, betas, eps):
+    """Second moments down to float32's subnormal range beside an eps of any size, 8-bit moments, whole tiles."""
+    n = 2048
+    g = A.f32(np.random.default_rng(3).standard_normal(n) * size * np.exp2(np.repeat([0, -20, -3, 0], 512)))
+    opt = S.AdamW([torch.ones(n, device="cuda")], bits=8, seed=2)
+    S.adamw_step(opt, [dev(g.astype(np.float32))], LR, *betas, eps)
+    m, v, r = A.moments(np.zeros(n), np.zeros(n), g, *betas)
+    rnd = A.rounding_bits(n, 0, 2, 1)
+    for x, t, col in ((m, opt.m[0], 0), (r, opt.v[0], 1)):
+        c, b = A.encode(x, rnd)
+        assert np.array_equal(bits(t), c) and np.array_equal(opt.scales[0].cpu().numpy()[:, col], b)
+    u = A.direction(m, r, 1, *betas, eps)
+    w = 1.0 - LR * u
+    assert np.all(np.abs(f64(opt.W[0]) - w) <= U * (2 * np.abs(w) + 20 * LR * np.abs(u)))
+
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_two_weights_in_one_matrix(eight):
     """Column halves of one matrix as two weights of a call."""
@@ -517,6 +565,14 @@ def test_norm_of_many_tensors_with_strides():
     G += [big[:, 1:38], torch.randn(64, 128, device="cuda", generator=g)[:, 64:], torch.randn(12, 10, device="cuda").to(BF16)[:, 1:2],
           torch.randn(1001, device="cuda", generator=g)[1:]]
     check_norm(G, 1.0)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("r,c,ld,off", [(1, 9001, 9001, 1), (300, 37, 41, 0), (40, 256, 264, 8), (40, 256, 264, 4), (5000, 1, 3, 1)])
+def test_norm_off_the_vector_addresses(r, c, ld, off, dt):
+    buf = torch.randn(r * ld + off + 8, device="cuda").to(dt)
+    buf[:off] = math.nan
+    check_norm([buf[off:off + r * ld].view(r, ld)[:, :c]], 1.0)
 
 
 @pytest.mark.parametrize("size", [1e-42, 1e-30, 1e-22, 1e17, 1e19, 1e30])
