@@ -452,31 +452,32 @@ def smuon_harness_gaussian(G, workers: int, stream_desc: GradStream, step: int, 
 _DT_TENSOR = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
 
 
+_NO_TENSOR = (0, 0, 0, 0, F32, 0)
+
+
 def _describe(t):
-    """(data, rows, cols, ld, dtype) of a tensor of any shape: contiguous, or 2-D with unit column stride."""
+    """(data, rows, cols, ld, dtype, 0) of a tensor of any shape: contiguous, or 2-D with unit column stride."""
     dt = _DT_TENSOR.get(t.dtype)
     if dt is None:
         raise ValueError(f"dtype {t.dtype} is not supported")
-    n = t.numel()
+    shape, n = t.shape, t.numel()
     if n == 0:
-        return 0, 0, 0, 0, dt
+        return 0, 0, 0, 0, dt, 0
     if t.is_contiguous():
-        cols = t.shape[-1] if t.dim() else 1
-        if max(cols, n // cols) >= 1 << 31:
+        cols = shape[-1] if shape else 1
+        rows = n // cols
+        if cols >= 1 << 31 or rows >= 1 << 31:
             raise ValueError("at most 2^31 - 1 rows and columns: view the tensor in another shape")
-        return t.data_ptr(), n // cols, cols, cols, dt
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        return t.data_ptr(), rows, cols, cols, dt, 0
+    if len(shape) != 2 or (t.stride(1) != 1 and shape[1] > 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
         raise ValueError("tensors must be contiguous, or 2-D with unit column stride and rows that do not overlap")
-    return t.data_ptr(), t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1], dt
+    return t.data_ptr(), shape[0], shape[1], t.stride(0) if shape[0] > 1 else shape[1], dt, 0
 
 
 def tensor(t) -> SmuonMat:
     """Describes a tensor for the AdamW calls: contiguous of any shape, or 2-D with unit column stride."""
-    ptr, rows, cols, ld, dt = _describe(t)
+    ptr, rows, cols, ld, dt, _ = _describe(t)
     return SmuonMat(ptr or None, rows, cols, ld, dt)
-
-
-_MAT = struct.Struct("@QiiqiI")  # SmuonMat
 
 
 def _tensors(ts, shapes=None, name="G"):
@@ -487,10 +488,10 @@ def _tensors(ts, shapes=None, name="G"):
         for i, (t, s) in enumerate(zip(ts, shapes)):
             if t is not None and t.shape != s:
                 raise ValueError(f"{name}[{i}] has shape {tuple(t.shape)}, its weight {tuple(s)}")
-    arr = (SmuonMat * len(ts))()
-    for i, t in enumerate(ts):  # packed in place: a SmuonMat object for each takes twice as long
-        if t is not None:
-            _MAT.pack_into(arr, i * _MAT.size, *_describe(t), 0)
+    arr, flat = (SmuonMat * len(ts))(), []
+    for t in ts:
+        flat += _describe(t) if t is not None else _NO_TENSOR
+    struct.pack_into("@" + "QiiqiI" * len(ts), arr, 0, *flat)  # the fields of each SmuonMat and its padding, at once
     return arr
 
 
