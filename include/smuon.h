@@ -495,8 +495,8 @@ smuon_status lionmuon_step(lionmuon_state* st, int32_t P, float beta1, float bet
  * b2 = 0.999 its root moves by 0.05% in a step, a code step is 6 to 12%. The
  * random bits of entry e of tensor i (one number for both moments) are half
  * e % 2 of word (e % 8) / 2 of Philox4x32-10 at counter (e / 8 low word, e / 8
- * high word, t, 1), key (seed, i): a run is a function of its inputs and its
- * seed. W' uses m' and r' before they are rounded to 8 bits.
+ * high word, low word of t, 1), key (seed, i): a run is a function of its inputs
+ * and its seed. W' uses m' and r' before they are rounded to 8 bits.
  *
  * Non-finite gradients make their entries' W and moments (8 bits: the moments
  * of their block) non-finite; d_skip_if with smuon_grad_norm drops such steps.

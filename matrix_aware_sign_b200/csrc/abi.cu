@@ -1396,7 +1396,7 @@ struct AdExec {
   DevInfo di;
 };
 
-const char* adamw_name(int kind) { return kind & AD_8BIT ? "k_adamw_8bit" : "k_adamw_32bit"; }
+const char* adamw_name(int kind) { return kind & AD_8BIT ? "k_adamw8" : "k_adamw32"; }
 
 // shapes and types of a state's moments, weights and masters; *eight: 8-bit moments
 smuon_status check_state(const adamw_state* st, bool* eight) {

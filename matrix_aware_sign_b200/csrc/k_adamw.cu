@@ -251,7 +251,7 @@ template <class Table>
 struct Walk {
   int b, stop;          // tile, and where the walk stops
   int li = 0, end = 0;  // the tile's tensor, and the first tile after that tensor
-  int which = 1;        // of the warp's two places in shared memory for tensors of a table in memory, taken in turn
+  int which = 1;        // of the warp's two places in shared memory for tensors of a table in memory, taken in turn (0 first)
   __device__ __forceinline__ Walk(int first, int after) : b(first), stop(after) {}
   __device__ __forceinline__ bool seek(const Table& tb, AdTensor* slots) {
     if (b >= stop) return false;
@@ -808,7 +808,7 @@ __device__ __forceinline__ void advance(const AdHyper& h, int skip) {
 constexpr int kAd32Warps = 4;
 template <int kKind, class Table>
 __global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_constant__ Table tb, const __grid_constant__ AdHyper h) {
-  __shared__ AdTensor slots[kAd32Warps][2];
+  __shared__ AdTensor slots[kAd32Warps][1];  // a warp looks up one tensor
   follow_previous();
   const int skip = h.skip ? *h.skip : 0;
   const Consts c = consts_of(h);

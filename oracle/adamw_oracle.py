@@ -114,12 +114,14 @@ def decode(codes, byte):
     return f32(np.where(per == 0, 0.0 * val, np.where(per == 255, math.nan, val)))
 
 
-def rounding_bits(n, tensor, seed, t):
-    """The 16 random bits of entries 0..n-1 of a tensor at step t (Philox4x32-10 in Python integers)."""
+def rounding_bits(n, tensor, seed, t, first=0):
+    """The 16 random bits of entries first..first + n - 1 (first a multiple of 8) of a tensor at step t
+    (Philox4x32-10 in Python integers)."""
     low = 0xFFFFFFFF
     out = np.empty(-(-n // 8) * 8, np.uint32)
     for e in range(-(-n // 8)):
-        c, k = [e & low, e >> 32, t & low, 1], [seed & low, tensor & low]
+        grp = first // 8 + e
+        c, k = [grp & low, grp >> 32, t & low, 1], [seed & low, tensor & low]
         for r in range(10):
             if r:
                 k = [(k[0] + 0x9E3779B9) & low, (k[1] + 0xBB67AE85) & low]

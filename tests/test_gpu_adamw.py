@@ -463,6 +463,118 @@ def test_steps_on_another_stream():
         r.check(opt, i, w2, tol + tol2 + U * np.abs(w2))
 
 
+def test_a_plan_runs_on_another_stream_at_once():
+    """A plan's table is uploaded on the stream that was current at its creation; the first run elsewhere waits for it
+    (here behind a queue of copies), and so does the norm's."""
+    shapes = [(300 + i,) for i in range(40)]
+    a, b = (make(shapes, True, F32, F32, False) for _ in range(2))
+    big = torch.randn(1 << 27, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        big.mul_(1.0)
+    plan, norm = S.AdamWPlan(a[0], a[1], B1, B2, EPS), S.GradNorm(a[1], 1.0)
+    plan.run(LR, stream=side)
+    norm.run(stream=side)
+    with torch.cuda.stream(side):
+        plan.run(LR)
+        norm.run()
+    for _ in range(2):
+        S.adamw_step(b[0], b[1], LR, B1, B2, EPS)
+    torch.cuda.synchronize()
+    want, _ = A.grad_norm(b[3], 1.0)
+    assert abs(float(norm.norm) - want) <= 6 * U * want
+    for k in ("W", "scales"):
+        assert all(torch.equal(x, y) for x, y in zip(getattr(a[0], k), getattr(b[0], k)))
+    for k in ("m", "v"):
+        assert all(np.array_equal(bits(x), bits(y)) for x, y in zip(getattr(a[0], k), getattr(b[0], k)))
+
+
+def test_plans_are_prepared_before_a_capture():
+    w, g = [torch.zeros(8, device="cuda")], [torch.ones(8, device="cuda")]
+    opt = S.AdamW(w, device_step=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="capture"):
+            S.AdamWPlan(opt, g)
+        S.adamw_step(opt, g, LR)
+    graph.replay()
+    graph.replay()
+    assert opt.t == 2
+
+
+def test_two_graphs_with_a_plan_each():
+    """Two captured steps on two states, replayed at the same time on two streams: plans share nothing."""
+    sets = [make([(50_001,), (130, 64)] + [(33,)] * 20, True, BF16, F32, True, seed=i, device_step=True) for i in (0, 1)]
+    twins = [make([(50_001,), (130, 64)] + [(33,)] * 20, True, BF16, F32, True, seed=i, device_step=True) for i in (0, 1)]
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for opt, G, _, _ in sets:
+        norm = S.GradNorm(G, 0.5)
+        plan = S.AdamWPlan(opt, G, B1, B2, EPS, grad_scale=norm.coef, skip_if=norm.skip)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            norm.run()
+            plan.run(LR)
+        graphs.append((g, norm, plan))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (g, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (opt, _, _, _), (other, G, _, _) in zip(sets, twins):
+        out, skip = torch.zeros(2, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        for _ in range(4):
+            keep = S.smuon_grad_norm(G, 0.5, out, skip)
+            S.adamw_step(other, G, LR, B1, B2, EPS, grad_scale=out[1:], skip_if=skip)
+        torch.cuda.synchronize()
+        del keep
+        assert opt.t == other.t == 4
+        for k in ("W", "m", "v", "master", "scales"):
+            for x, y in zip(getattr(opt, k), getattr(other, k)):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_offsets_beyond_32_bits(eight):
+    """More than 2^31 entries in one tensor: its start, the 2^31 border and its end against the reference, and the norm."""
+    rows, cols = 2, (1 << 30) + 777
+    n = rows * cols
+    if torch.cuda.mem_get_info()[0] < (14 if eight else 27) * n // 2 + (2 << 30):
+        pytest.skip("needs more free memory")
+    W = torch.full((rows, cols), 0.5, dtype=BF16, device="cuda")
+    G = torch.full((rows, cols), 2.0 ** -9, dtype=BF16, device="cuda")
+    flat_w, flat_g = W.view(-1), G.view(-1)
+    places = [0, (1 << 31) - 512, (1 << 31), (n // 256 - 1) * 256]
+    rng = np.random.default_rng(1)
+    for p in places:
+        size = min(512, n - p)
+        flat_g[p:p + size] = dev((rng.standard_normal(size) * 1e-2).astype(np.float32)).to(BF16)
+    opt = S.AdamW([W], bits=8 if eight else 32, weight_decay=WD, seed=6)
+    S.adamw_step(opt, [G], LR, B1, B2, EPS)
+    for p in places:
+        size = min(512, n - p)
+        g, z = f64(flat_g[p:p + size]), np.zeros(size)
+        m, v, r = A.moments(z, z, g, B1, B2)
+        w = 0.5 - LR * (WD * 0.5 + A.direction(m, r, 1, B1, B2, EPS))
+        assert np.all(np.abs(f64(flat_w[p:p + size]) - w) <= (2.0 ** -8 + 2.0 ** -20) * np.abs(w))
+        sl = slice(p, p + size)
+        if eight:
+            rnd = A.rounding_bits(size, 0, 6, 1, first=p)
+            for x, t, col in ((m, opt.m[0], 0), (r, opt.v[0], 1)):
+                c, b = A.encode(x, rnd)
+                assert np.array_equal(bits(t.view(-1)[sl]), c)
+                assert np.array_equal(opt.scales[0][p // 256:p // 256 + b.size, col].cpu().numpy(), b)
+        else:
+            assert np.array_equal(f64(opt.m[0].view(-1)[sl]), m) and np.array_equal(f64(opt.v[0].view(-1)[sl]), v)
+    norm = S.GradNorm([G], 1.0)
+    norm.run()
+    # the places' gradients in place of as many of 2^-9
+    taken = sum(min(512, n - p) for p in places)
+    want = math.sqrt(sum(float((f64(flat_g[p:p + min(512, n - p)]) ** 2).sum()) for p in places) + (n - taken) * 2.0 ** -18)
+    assert abs(float(norm.norm) - want) <= 6 * U * want
+
+
 def test_results_do_not_depend_on_the_split():
     """The same tensors in one call, one by one in calls of their own (32 bits), and prepared: equal bits."""
     shapes = [(257,), (40, 41), (3000,)]
