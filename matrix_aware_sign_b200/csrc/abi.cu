@@ -1456,6 +1456,19 @@ void split_tensors(const std::vector<AdTensor>& ts, size_t most, F&& part) {
     i = j;
   }
 }
+// the guide of a table of n tensors with `total` tiles
+template <class Tensor>
+Guide guide_of(const Tensor* t, int32_t n, int32_t total) {
+  Guide g{};
+  while (((int64_t)total - 1) >> g.shift >= Guide::kParts) ++g.shift;
+  int32_t li = 0;
+  for (int k = 0; k <= Guide::kParts; ++k) {
+    const int64_t tile = std::min<int64_t>((int64_t)k << g.shift, (int64_t)total - 1);
+    while (li + 1 < n && t[li + 1].tile_begin <= tile) ++li;
+    g.at[k] = li;
+  }
+  return g;
+}
 size_t adamw_ws_bytes(int64_t n_tensors) { return (size_t)round_up(std::max<int64_t>(n_tensors * (int64_t)sizeof(AdTensor), 256), 256); }
 
 smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double beta1, double beta2, double eps,
@@ -1526,7 +1539,9 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
       if (in_ws) {
         table.resize(first + (j - i));
         dst = table.data() + first;
-        P.dev = AdDevTable{(int32_t)(j - i), tiles, reinterpret_cast<const AdTensor*>(ws) + first};
+        P.dev.n_tensors = (int32_t)(j - i);
+        P.dev.total_tiles = tiles;
+        P.dev.t = reinterpret_cast<const AdTensor*>(ws) + first;
       } else if (j - i <= (size_t)kAdFew) {
         P.small.reset(new AdTable<kAdFew>());
         P.small->n_tensors = (int32_t)(j - i);
@@ -1545,6 +1560,7 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
         begin += (int32_t)tiles_of(ts[i].n);
         P.bytes += per * (double)ts[i].n + (eight ? 4.0 * (double)blocks_of(ts[i].n) : 0.0);
       }
+      if (in_ws) P.dev.guide = guide_of(table.data() + first, P.dev.n_tensors, tiles);
       ex->parts.push_back(std::move(P));
     });
   }
@@ -1662,6 +1678,7 @@ smuon_status prepare_norm(const smuon_mat* G, int32_t n, double max_norm, float*
   ex->a.t = reinterpret_cast<const NormTensor*>(base + kNormHead);
   ex->a.n_tensors = used;
   ex->a.total_tiles = (int32_t)tiles;
+  ex->a.guide = guide_of(t, used, (int32_t)tiles);
   ex->a.partials = reinterpret_cast<double*>(base + bytes.size());
   ex->a.arrived = reinterpret_cast<uint32_t*>(base);
   ex->a.max_norm = max_norm;

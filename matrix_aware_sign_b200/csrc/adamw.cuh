@@ -53,9 +53,17 @@ struct AdTable {
   int32_t n_tensors, total_tiles;
   AdTensor t[kCap];
 };
+// Where to look in a table in memory: the tensor of each 2^shift-th tile, and of the last. It travels with the launch, so
+// that finding a tile's tensor takes one load from the table instead of two (and none inside a large tensor).
+struct Guide {
+  static constexpr int kParts = 64;
+  int32_t shift;
+  int32_t at[kParts + 1];
+};
 struct AdDevTable {
   int32_t n_tensors, total_tiles;
   const AdTensor* t;
+  Guide guide;
 };
 
 enum AdKind { AD_W_F32 = 0, AD_W_BF16 = 1, AD_W_MASTER = 2, AD_G_BF16 = 4, AD_8BIT = 8, AD_KINDS = 16 };
@@ -76,6 +84,7 @@ constexpr int kNormMaxGrid = 592;  // four CTAs an SM (64 registers a thread)
 struct NormArgs {
   const NormTensor* t;
   int32_t n_tensors, total_tiles;
+  Guide guide;
   double* partials;   // one per CTA
   uint32_t* arrived;  // zero before a launch, and after it
   double max_norm;

@@ -231,11 +231,12 @@ __device__ __forceinline__ int tensor_of(const Table& tb, int b, int li) {
   }
   return lo;
 }
-// in a table in memory: the warp looks at 32 places at once, so a thousand tensors take two loads
+// in a table in memory: between two places of the guide, the warp looking at 32 tensors at once
 template <class Tensor>
-__device__ __forceinline__ int tensor_of_warp(const Tensor* t, int n, int b, int li) {
-  const int lane = threadIdx.x & 31;
-  for (int len = n - li; len > 1;) {
+__device__ __forceinline__ int tensor_of_warp(const Tensor* t, const Guide& guide, int b) {
+  const int part = b >> guide.shift, lane = threadIdx.x & 31;
+  int li = guide.at[part];
+  for (int len = guide.at[part + 1] - li + 1; len > 1;) {
     const int step = (len + 31) >> 5, at = li + lane * step;
     const bool ok = lane * step < len && t[at].tile_begin <= b;
     const int k = __popc(__ballot_sync(0xffffffffu, ok)) - 1;
@@ -244,7 +245,7 @@ __device__ __forceinline__ int tensor_of_warp(const Tensor* t, int n, int b, int
   }
   return li;
 }
-__device__ __forceinline__ int tensor_of(const AdDevTable& tb, int b, int li) { return tensor_of_warp(tb.t, tb.n_tensors, b, li); }
+__device__ __forceinline__ int tensor_of(const AdDevTable& tb, int b, int) { return tensor_of_warp(tb.t, tb.guide, b); }
 
 // A warp's walk over the tiles of a launch.
 template <class Table>
@@ -1076,7 +1077,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_norm(const __grid_constant__ No
   const int stop = (int)((int64_t)a.total_tiles * (blockIdx.x + 1) / gridDim.x);
   for (int b = (int)((int64_t)a.total_tiles * blockIdx.x / gridDim.x) + (threadIdx.x >> 5); b < stop; b += 8) {
     if (b >= end) {
-      li = tensor_of_warp(a.t, a.n_tensors, b, li);
+      li = tensor_of_warp(a.t, a.guide, b);
       const NormTensor& T = a.t[li];
       A = NormAt{T.g, T.n, T.tile_begin, T.vec && T.ld == T.cols};
       bf16 = T.bf16;
