@@ -833,8 +833,9 @@ __global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_con
 // Each warp has two stages of its own: the next tile's operands are on their way into one (cp.async) while the other is
 // stepped. A CTA walks over a stretch of its own: tiles dealt out in turn over the grid took 2.35 ms instead of 2.20 on
 // the 774M-entry case with master (all CTAs load and store in step). Deeper rings (up to four stages: 2.35, 2.47 and 2.51
-// ms with two, three and four) and more warps with fewer registers measured slower. The pipes of the arithmetic are what
-// is left on bf16 weights without a master (issue slots 65% busy, integer pipe 51%, HBM 54%; 65.6M entries: 134 to 141 us).
+// ms with two, three and four) and more warps with fewer registers measured slower. bf16 weights without a
+// master are bound by issue slots and HBM together: 65.6M entries take 134 to 141 us (4.7 to 4.9 TB/s), data that stays
+// in L2 would take 114 with the issue slots 78% busy.
 constexpr int kAd8Warps = 2, kAd8Ctas = 8;
 constexpr int kAd8Run = 24;  // tiles of a warp in a long run of CTAs
 template <int kKind, class Table>

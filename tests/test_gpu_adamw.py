@@ -490,6 +490,33 @@ def test_a_plan_runs_on_another_stream_at_once():
         assert all(np.array_equal(bits(x), bits(y)) for x, y in zip(getattr(a[0], k), getattr(b[0], k)))
 
 
+def test_a_plan_made_on_a_side_stream_runs_on_the_default_one():
+    a, b = (make([(300 + i,) for i in range(40)], False, F32, F32, False) for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    big = torch.randn(1 << 27, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big.mul_(1.0)
+        plan, norm = S.AdamWPlan(a[0], a[1], B1, B2, EPS), S.GradNorm(a[1], 1.0)
+    plan.run(LR)
+    norm.run()
+    S.adamw_step(b[0], b[1], LR, B1, B2, EPS)
+    torch.cuda.synchronize()
+    for k in ("W", "m", "v"):
+        assert all(torch.equal(x, y) for x, y in zip(getattr(a[0], k), getattr(b[0], k)))
+    assert abs(float(norm.norm) - A.grad_norm(a[3], 1.0)[0]) <= 6 * U * float(norm.norm)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_one_gradient_for_two_weights(eight):
+    opt, G, refs, gs = make([(700,), (700,), (9, 40)], eight, F32, BF16, False)
+    G[1], gs[1] = G[0], gs[0]
+    S.adamw_step(opt, G, LR, B1, B2, EPS)
+    step_refs(opt, refs, gs, 1)
+
+
 def test_plans_are_prepared_before_a_capture():
     w, g = [torch.zeros(8, device="cuda")], [torch.ones(8, device="cuda")]
     opt = S.AdamW(w, device_step=True)
