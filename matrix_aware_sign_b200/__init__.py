@@ -5,8 +5,9 @@ CUDA kernels. PyTorch supplies device memory and the current stream. There is
 no fallback: if the shared library is missing, importing a function raises.
 
 Functions keep the C names: smuon_ns, smuon_sign_pack, smuon_vote,
-smuon_update, cachemuon_reuse_probe, lionmuon_step (plus the workspace
-queries). Matrices are 2-D torch tensors with unit column stride.
+smuon_update, cachemuon_reuse_probe, lionmuon_step, adamw_step, adamw_convert,
+smuon_grad_norm (plus the workspace queries). Matrices are 2-D torch tensors
+with unit column stride; the AdamW calls take tensors of any shape.
 """
 from __future__ import annotations
 
@@ -622,7 +623,8 @@ class _Prepared:
 
     def _follow(self, s):
         if not torch.cuda.is_current_stream_capturing():  # a capture begins after all that was uploaded before it
-            torch.cuda.ExternalStream(s).wait_event(self._ready)
+            # (handle 0 is the default stream; ExternalStream(0) would be a new one)
+            (torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream(self._index)).wait_event(self._ready)
             self._seen.add(s)
 
     def __del__(self):

@@ -291,14 +291,16 @@ def test_two_weights_in_one_matrix(eight):
         ref.check(opt, i, *ref.step(f64(G[i]), 1))
 
 
+@pytest.mark.parametrize("planned", [False, True])
 @pytest.mark.parametrize("eight", [False, True])
-def test_many_tensors_mixed_types_and_empty_ones(eight):
-    """More tensors than a launch holds, of every combination of types, empty ones among them: each tensor keeps its own
-    place in the lists (the rounding's key), its own decay and learning-rate factor."""
+def test_many_tensors_mixed_types_and_empty_ones(eight, planned):
+    """More tensors than a launch holds, of every combination of types, empty ones and a long one among them: each tensor
+    keeps its own place in the lists (the rounding's key), its own decay and learning-rate factor. Planned: the tables in
+    memory, some hundred tensors each."""
     rng = np.random.default_rng(6)
     W, G, M, refs, gs, wd, ls = [], [], [], [], [], [], []
     for i in range(700):
-        n = 0 if i % 50 == 7 else int(rng.integers(1, 600))
+        n = 0 if i % 50 == 7 else 40_000 + i if i in (100, 401) else int(rng.integers(1, 600))
         wdt, gdt = (F32, BF16)[int(rng.integers(2))], (F32, BF16)[int(rng.integers(2))]
         w, g, m, v = draw_tensor(rng, (n,))
         W.append(torch.from_numpy(w.astype(np.float32)).to(wdt).cuda())
@@ -309,12 +311,34 @@ def test_many_tensors_mixed_types_and_empty_ones(eight):
         refs.append(Reference(f64(W[-1]), np.zeros(n), np.zeros(n), eight, i, 9, wd[-1], ls[-1], wdt == BF16, M[-1] is not None))
         gs.append(f64(G[-1]))
     opt = S.AdamW(W, bits=8 if eight else 32, master=M, weight_decay=wd, lr_scale=ls, seed=9, device_step=True)
+    plan = S.AdamWPlan(opt, G, B1, B2, EPS) if planned else None
     for t in (1, 2):
-        S.adamw_step(opt, G, LR, B1, B2, EPS)
+        plan.run(LR) if planned else S.adamw_step(opt, G, LR, B1, B2, EPS)
         assert opt.d_t.tolist() == [t, 0]
         for i, (r, g) in enumerate(zip(refs, gs)):
             if g.size:
                 r.check(opt, i, *r.step(g, t))
+
+
+def test_a_plan_of_two_thousand_tensors():
+    """One type, lengths from one entry to several tiles: the guide's parts hold more than 32 tensors and less than one."""
+    rng = np.random.default_rng(9)
+    ns = [int(x) for x in np.exp(rng.uniform(0, 5, 1000))] + [70_000] + [int(x) for x in np.exp(rng.uniform(0, 9, 1000))]
+    W = [torch.randn(n, device="cuda") for n in ns]
+    G = [torch.randn(n, device="cuda") for n in ns]
+    for b in (32, 8):
+        one = S.AdamW([w.clone() for w in W], bits=b, weight_decay=WD, seed=3)
+        two = S.AdamW([w.clone() for w in W], bits=b, weight_decay=WD, seed=3)
+        S.AdamWPlan(one, G, B1, B2, EPS).run(LR)
+        S.adamw_step(two, G, LR, B1, B2, EPS)
+        for k in ("W", "m", "v", "scales"):
+            for x, y in zip(getattr(one, k) or [], getattr(two, k) or []):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    for i in (0, 999, 1000, 2000):  # and some of them against the reference
+        g, z = f64(G[i]), np.zeros(ns[i])
+        m, v, r = A.moments(z, z, g, B1, B2)
+        c, byte = A.encode(m, A.rounding_bits(ns[i], i, 3, 1))
+        assert np.array_equal(bits(one.m[i]), c) and np.array_equal(one.scales[i][:, 0].cpu().numpy(), byte)
 
 
 def test_only_empty_tensors():
@@ -507,6 +531,32 @@ def test_a_plan_made_on_a_side_stream_runs_on_the_default_one():
     for k in ("W", "m", "v"):
         assert all(torch.equal(x, y) for x, y in zip(getattr(a[0], k), getattr(b[0], k)))
     assert abs(float(norm.norm) - A.grad_norm(a[3], 1.0)[0]) <= 6 * U * float(norm.norm)
+
+
+def test_events_order_what_a_kernel_reads():
+    """A stream that waits for another one's event between two of these kernels (the first of which lets the next begin
+    early): the second reads what the other stream wrote before the event."""
+    n = 1 << 20
+    g, ones = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    big = torch.randn(1 << 27, device="cuda")
+    first, norm = S.GradNorm([ones], 1.0), S.GradNorm([g], 1.0)
+    opt = S.AdamW([torch.zeros(n, device="cuda")])
+    step = S.AdamWPlan(opt, [g], B1, 0.0, EPS)
+    side = torch.cuda.Stream()
+    for i in range(1, 9):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(10):
+                big.mul_(1.0)
+            g.fill_(float(i))
+            ready = torch.cuda.Event()
+            ready.record()
+        first.run()
+        torch.cuda.current_stream().wait_event(ready)
+        norm.run()
+        step.run(0.0)
+        torch.cuda.synchronize()
+        assert float(norm.norm) == i * 1024.0 and float(opt.v[0][n - 1]) == float(i * i)
 
 
 @pytest.mark.parametrize("eight", [False, True])
