@@ -202,9 +202,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current device and a device's current stream as bare numbers (a CPU-only PyTorch has neither)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:  # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -621,6 +626,13 @@ class _Prepared:
         self._ready, self._seen = torch.cuda.Event(), {self._made}
         self._ready.record()
 
+    def _here(self, stream):
+        """Handle of the stream to run on, which follows the upload. The plan's device is current."""
+        s = _raw_stream(self._index) if stream is None else _stream(stream)
+        if s not in self._seen:
+            self._follow(s)
+        return s
+
     def _follow(self, s):
         if not torch.cuda.is_current_stream_capturing():  # a capture begins after all that was uploaded before it
             # (handle 0 is the default stream; ExternalStream(0) would be a new one)
@@ -652,17 +664,17 @@ class AdamWPlan(_Prepared):
                                            _stream(None), ctypes.byref(h)))
             self._uploaded()
         self.handle, self._state, self._device_lr = h, ctypes.byref(opt.state), d_lr is not None
+        self._execute = lib().adamw_execute
 
     def run(self, lr=None, stream=None):
         if (lr is None) != self._device_lr:
             raise ValueError("give lr once: as a device tensor to the plan, or as a number here")
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.run(lr, stream)
-        s = _stream(stream)
-        if s not in self._seen:
-            self._follow(s)
-        _check(lib().adamw_execute(self.handle, self._state, 0.0 if lr is None else lr, s))
+        code = self._execute(self.handle, self._state, 0.0 if lr is None else lr, self._here(stream))
+        if code:
+            _check(code)
 
 
 def adamw_convert(src: AdamW, dst: AdamW, stream=None):
@@ -701,16 +713,15 @@ class GradNorm(_Prepared):
                                                      self.skip.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
                                                      _ptr(status), _stream(None), ctypes.byref(h)))
             self._uploaded()
-        self.handle = h
+        self.handle, self._execute = h, lib().smuon_grad_norm_execute
 
     def run(self, stream=None):
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.run(stream)
-        s = _stream(stream)
-        if s not in self._seen:
-            self._follow(s)
-        _check(lib().smuon_grad_norm_execute(self.handle, s))
+        code = self._execute(self.handle, self._here(stream))
+        if code:
+            _check(code)
 
 
 def smuon_grad_norm(G, max_norm: float, out, skip=None, ws=None, status=None, stream=None):
