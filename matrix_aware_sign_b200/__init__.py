@@ -611,7 +611,8 @@ def adamw_step(opt: AdamW, G, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=N
 
 class _Prepared:
     """A plan whose table was uploaded on the stream that was current then. Runs on that stream follow the upload by
-    themselves; the first run on another stream waits for it."""
+    themselves; the first run on another stream waits for it. A graph that captured a run needs the plan as long as it
+    is replayed."""
     handle = None
 
     def _uploading(self, device):
@@ -621,9 +622,8 @@ class _Prepared:
         self._index = device.index
         return torch.cuda.device(device)
 
-    def _uploaded(self):
-        self._made = _stream(None)
-        self._ready, self._seen = torch.cuda.Event(), {self._made}
+    def _uploaded(self, *own):
+        self._own, self._ready, self._seen = own, torch.cuda.Event(), {_stream(None)}
         self._ready.record()
 
     def _here(self, stream):
@@ -634,10 +634,14 @@ class _Prepared:
         return s
 
     def _follow(self, s):
-        if not torch.cuda.is_current_stream_capturing():  # a capture begins after all that was uploaded before it
-            # (handle 0 is the default stream; ExternalStream(0) would be a new one)
-            (torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream(self._index)).wait_event(self._ready)
-            self._seen.add(s)
+        if torch.cuda.is_current_stream_capturing():  # a capture begins after all that was uploaded before it
+            return
+        # (handle 0 is the default stream; ExternalStream(0) would be a new one)
+        stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream(self._index)
+        stream.wait_event(self._ready)
+        for t in self._own:  # allocated on the stream of the creation: not reused before this one is done with them
+            t.record_stream(stream)
+        self._seen.add(s)
 
     def __del__(self):
         h = self.handle
@@ -662,7 +666,7 @@ class AdamWPlan(_Prepared):
             _check(lib().adamw_plan_create(ctypes.byref(opt.state), mats, beta1, beta2, eps, _ptr(d_lr),
                                            _ptr(grad_scale), _ptr(skip_if), self.ws.data_ptr(), self.ws.numel(),
                                            _stream(None), ctypes.byref(h)))
-            self._uploaded()
+            self._uploaded(self.ws)
         self.handle, self._state, self._device_lr = h, ctypes.byref(opt.state), d_lr is not None
         self._execute = lib().adamw_execute
 
@@ -712,7 +716,7 @@ class GradNorm(_Prepared):
             _check(lib().smuon_grad_norm_plan_create(mats, len(G), max_norm, self.out.data_ptr(),
                                                      self.skip.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
                                                      _ptr(status), _stream(None), ctypes.byref(h)))
-            self._uploaded()
+            self._uploaded(self.ws, self.out, self.skip)
         self.handle, self._execute = h, lib().smuon_grad_norm_execute
 
     def run(self, stream=None):

@@ -1305,13 +1305,13 @@ smuon_status check_tensor(const smuon_mat& a, const char* what, int i, int32_t d
   if (a.rows < 0 || a.cols < 0) return fail(SMUON_ERR_SHAPE, "%s[%d] has shape %dx%d", what, i, a.rows, a.cols);
   if (a.dtype != d0 && a.dtype != d1) return fail(SMUON_ERR_DTYPE, "%s[%d] has an unsupported dtype %d", what, i, a.dtype);
   if (a.ld < a.cols) return fail(SMUON_ERR_SHAPE, "%s[%d].ld=%lld < cols=%d", what, i, (long long)a.ld, a.cols);
-  if (a.ld > ((int64_t)1 << 40)) return fail(SMUON_ERR_SHAPE, "%s[%d].ld=%lld is too large", what, i, (long long)a.ld);
   if (!strided && a.rows > 1 && a.ld != a.cols)
     return fail(SMUON_ERR_SHAPE, "%s[%d] must be contiguous (ld=%lld, cols=%d)", what, i, (long long)a.ld, a.cols);
   const int64_t n = (int64_t)a.rows * a.cols;
-  if (n > ((int64_t)1 << 38)) return fail(SMUON_ERR_SHAPE, "%s[%d] has more than 2^38 entries", what, i);
+  if (n > ((int64_t)1 << 38) || (double)a.rows * (double)a.ld > 0x1p40)
+    return fail(SMUON_ERR_SHAPE, "%s[%d] has more than 2^38 entries or spans more than 2^40", what, i);
   if (n && !a.data) return fail(SMUON_ERR_INVALID_ARG, "%s[%d].data is NULL", what, i);
-  if (reinterpret_cast<uintptr_t>(a.data) % dtype_size(a.dtype) != 0)
+  if (reinterpret_cast<uintptr_t>(a.data) & (uintptr_t)(dtype_size(a.dtype) - 1))
     return fail(SMUON_ERR_INVALID_ARG, "%s[%d].data is not aligned to its element size", what, i);
   return SMUON_OK;
 }
@@ -1324,7 +1324,7 @@ bool has_stride(const smuon_mat& a) { return a.rows > 1 && a.ld != a.cols; }
 // whether every `k` (8 or 16) entries from a multiple of k on are aligned vectors: at most 32 bytes each, all in one row
 bool vec_of(const smuon_mat& a, int k) {
   const int bytes = std::min(32, k * dtype_size(a.dtype));
-  return reinterpret_cast<uintptr_t>(a.data) % bytes == 0 && (!has_stride(a) || (a.cols % k == 0 && a.ld % k == 0));
+  return (reinterpret_cast<uintptr_t>(a.data) & (uintptr_t)(bytes - 1)) == 0 && (!has_stride(a) || (a.cols % k == 0 && a.ld % k == 0));
 }
 
 // memory that a call reads or writes: rows of row_bytes, pitch bytes apart
@@ -1352,12 +1352,23 @@ bool meet(const Span& a, const Span& b) {
 }
 
 smuon_status check_overlap(std::vector<Span>& v) {
+  if (v.empty()) return SMUON_OK;
   // by address, from the runs that are in order already (a list of views of one buffer is one run)
   std::vector<size_t> runs{0};
   auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
-  for (size_t j = 1; j < v.size(); ++j)
+  bool apart = true;  // whether each run's spans lie one behind the other
+  for (size_t j = 1; j < v.size(); ++j) {
     if (before(v[j], v[j - 1])) runs.push_back(j);
+    else apart = apart && v[j - 1].hi <= v[j].lo;
+  }
   runs.push_back(v.size());
+  if (apart) {  // the common case: a buffer to each list. Then it is enough that the runs do not reach into one another
+    std::vector<std::pair<uintptr_t, uintptr_t>> ends;
+    for (size_t k = 0; k + 1 < runs.size(); ++k) ends.emplace_back(v[runs[k]].lo, v[runs[k + 1] - 1].hi);
+    std::sort(ends.begin(), ends.end());
+    for (size_t k = 1; k < ends.size(); ++k) apart = apart && ends[k - 1].second <= ends[k].first;
+    if (apart) return SMUON_OK;
+  }
   while (runs.size() > 2) {
     std::vector<size_t> merged{0};
     for (size_t k = 0; k + 2 < runs.size(); k += 2) {
@@ -1822,6 +1833,7 @@ smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* strea
     const adamw_state* s8 = to8 ? dst : src;
     std::vector<Span> spans;
     std::vector<ConvTensor> ts;
+    ts.reserve((size_t)src->n_tensors);
     for (int i = 0; i < src->n_tensors; ++i) {
       const int64_t n = entries(src->W[i]);
       if (entries(dst->W[i]) != n) return fail(SMUON_ERR_SHAPE, "tensor %d has %lld and %lld entries", i, (long long)n, (long long)entries(dst->W[i]));

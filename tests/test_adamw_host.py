@@ -162,6 +162,7 @@ REFUSED = {
     "negative decay": (dict(wd=-0.1), {}, -1, b"weight_decay[0]"),
     "nan lr scale": (dict(ls=math.nan), {}, -1, b"lr_scale[0]"),
     "negative rows": (dict(W=_m(0, rows=-1)), {}, -2, b"W[0]"),
+    "rows too far apart": ({}, dict(G=_m(3, ld=1 << 39)), -2, b"2^40"),
     "W null": (dict(W=S.SmuonMat(None, 4, 8, 8, S.F32)), {}, -1, b"NULL"),
     "W misaligned": (dict(W=_m(0, off=2)), {}, -1, b"aligned"),
     "G shape": ({}, dict(G=_m(3, rows=8, cols=4)), -2, b"G[0]"),
