@@ -924,7 +924,9 @@ template cudaError_t launch_adamw(int, const AdDevTable&, const AdHyper&, int, c
 // ---------------------------------------------------------------- gradient norm
 // A lane squares eight entries at a time: their sum in float32 (one rounding an entry), added up in float64 in a fixed
 // order. Where the float32 sum leaves [2^-90, 2^120] (squares that underflow or overflow, NaN, zeros) it is formed in
-// float64 instead, so every gradient whose norm float32 holds gets it.
+// float64 instead, so every gradient whose norm float32 holds gets it. It reads 2 or 4 bytes an entry and writes nothing:
+// 774M bf16 entries take 257 to 276 us (86 to 92% of the copy rate); 290 short tensors 5.6 us, which are latencies (table,
+// tensor, data, the CTAs' sums). One launch: the last CTA to arrive adds the others' sums, in their order.
 namespace {
 constexpr float kNormLow = 0x1p-90f, kNormHigh = 0x1p120f;
 __device__ __noinline__ double sumsq_f64(const float (&g)[8]) {
