@@ -610,35 +610,34 @@ def adamw_step(opt: AdamW, G, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=N
 
 
 class _Prepared:
-    """A plan whose table was uploaded on the stream that was current then. Runs on that stream follow the upload by
-    themselves; the first run on another stream waits for it. A graph that captured a run needs the plan as long as it
-    is replayed."""
+    """A plan with its table in device memory. Its creation returns when the table has arrived there (it waits for the
+    stream that was current then), so runs need no order against it: on any stream, captured or not. A graph that
+    captured a run needs the plan as long as it is replayed."""
     handle = None
 
     def _uploading(self, device):
-        """To be entered around the creation: its device, and no capture (the upload would be the graph's)."""
-        if torch.cuda.is_current_stream_capturing():
-            raise ValueError("prepare the plan before the capture: its table is uploaded once")
+        """To be entered around the creation: its device, and no capture there (the upload would be the graph's)."""
         self._index = device.index
+        with torch.cuda.device(device):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("prepare the plan before the capture: its table is uploaded once")
         return torch.cuda.device(device)
 
     def _uploaded(self, *own):
-        self._own, self._ready, self._seen = own, torch.cuda.Event(), {_stream(None)}
-        self._ready.record()
+        stream = torch.cuda.current_stream()
+        stream.synchronize()
+        self._own, self._seen = own, {stream.cuda_stream}
 
     def _here(self, stream):
-        """Handle of the stream to run on, which follows the upload. The plan's device is current."""
+        """Handle of the stream to run on. The plan's device is current."""
         s = _raw_stream(self._index) if stream is None else _stream(stream)
         if s not in self._seen:
-            self._follow(s)
+            self._hold(s)
         return s
 
-    def _follow(self, s):
-        if torch.cuda.is_current_stream_capturing():  # a capture begins after all that was uploaded before it
-            return
+    def _hold(self, s):
         # (handle 0 is the default stream; ExternalStream(0) would be a new one)
         stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream(self._index)
-        stream.wait_event(self._ready)
         for t in self._own:  # allocated on the stream of the creation: not reused before this one is done with them
             t.record_stream(stream)
         self._seen.add(s)

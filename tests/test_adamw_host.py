@@ -330,3 +330,26 @@ def test_checkpoint_knows_the_state():
     assert b.state.t == 4 and torch.equal(b.W[0], a.W[0])
     with pytest.raises(ValueError, match="seed"):
         C.restore(Fake(4), snap)
+
+
+def test_a_plan_asks_its_own_device_for_a_capture(monkeypatch):
+    """What counts is whether the stream of the plan's device is capturing, whichever device is current."""
+    class Device:
+        current = 0
+
+        def __init__(self, device):
+            self.to = device.index
+
+        def __enter__(self):
+            self.back, Device.current = Device.current, self.to
+
+        def __exit__(self, *_):
+            Device.current = self.back
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: Device.current == 1)
+    with pytest.raises(ValueError, match="capture"):
+        S._Prepared()._uploading(torch.device("cuda:1"))
+    assert Device.current == 0
+    with S._Prepared()._uploading(torch.device("cuda:0")):
+        assert Device.current == 0

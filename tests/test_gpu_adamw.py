@@ -533,6 +533,39 @@ def test_a_plan_made_on_a_side_stream_runs_on_the_default_one():
     assert abs(float(norm.norm) - A.grad_norm(a[3], 1.0)[0]) <= 6 * U * float(norm.norm)
 
 
+def test_a_plan_is_complete_when_it_is_made():
+    """A plan made behind a queue of work: its table has arrived when the constructor returns (checked before anything
+    runs on it), so a capture begun by hand, which waits for nothing, may be replayed at once."""
+    shapes = [(300 + i,) for i in range(40)]
+    a, b = (make(shapes, True, F32, F32, False, device_step=True) for _ in range(2))
+    big = torch.randn(1 << 27, device="cuda")
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big.mul_(1.0)
+        plan = S.AdamWPlan(a[0], a[1], B1, B2, EPS)
+        assert side.query()
+        for _ in range(20):
+            big.mul_(1.0)
+        norm = S.GradNorm(a[1], 1.0)
+        assert side.query()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(other):
+        graph.capture_begin()
+        plan.run(LR)
+        norm.run()
+        graph.capture_end()
+        graph.replay()
+    S.adamw_step(b[0], b[1], LR, B1, B2, EPS)
+    torch.cuda.synchronize()
+    for k in ("W", "m", "v", "scales"):
+        for x, y in zip(getattr(a[0], k), getattr(b[0], k)):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    want, _ = A.grad_norm(a[3], 1.0)
+    assert abs(float(norm.norm) - want) <= 6 * U * want
+
+
 def test_events_order_what_a_kernel_reads():
     """A stream that waits for another one's event between two of these kernels (the first of which lets the next begin
     early): the second reads what the other stream wrote before the event."""
