@@ -1327,7 +1327,7 @@ bool vec_of(const smuon_mat& a, int k) {
   return (reinterpret_cast<uintptr_t>(a.data) & (uintptr_t)(bytes - 1)) == 0 && (!has_stride(a) || (a.cols % k == 0 && a.ld % k == 0));
 }
 
-// memory that a call reads or writes: rows of row_bytes, pitch bytes apart
+// memory that a call reads or writes: rows of `row` bytes, `pitch` bytes apart where there are many, else one run
 struct Span {
   uintptr_t lo, hi, row, pitch;
   bool many, written;
@@ -1335,10 +1335,15 @@ struct Span {
   int i;
 };
 
+void add_run(std::vector<Span>& v, const void* p, uintptr_t bytes, bool written, const char* what, int i) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  v.push_back(Span{lo, lo + bytes, bytes, 0, false, written, what, i});
+}
 void add_span(std::vector<Span>& v, const smuon_mat& a, bool written, const char* what, int i) {
   if (entries(a) == 0) return;
   const uintptr_t es = dtype_size(a.dtype), p = reinterpret_cast<uintptr_t>(a.data);
-  v.push_back(Span{p, p + ((uintptr_t)(a.rows - 1) * a.ld + a.cols) * es, a.cols * es, (uintptr_t)a.ld * es, a.rows > 1,
+  if (!has_stride(a)) return add_run(v, a.data, (uintptr_t)entries(a) * es, written, what, i);
+  v.push_back(Span{p, p + ((uintptr_t)(a.rows - 1) * a.ld + a.cols) * es, a.cols * es, (uintptr_t)a.ld * es, true,
                    written, what, i});
 }
 
@@ -1451,8 +1456,7 @@ void add_moments(std::vector<Span>& v, const adamw_state* st, bool eight, bool w
   add_spans(v, st->v, st->n_tensors, written, "v");
   for (int i = 0; eight && i < st->n_tensors; ++i) {
     const int64_t n = entries(st->W[i]);
-    const uintptr_t p = reinterpret_cast<uintptr_t>(st->scales[i]);
-    if (n) v.push_back(Span{p, p + 2 * (uintptr_t)blocks_of(n), 0, 0, false, written, "scales", i});
+    if (n) add_run(v, st->scales[i], 2 * (uintptr_t)blocks_of(n), written, "scales", i);
   }
 }
 
@@ -1528,10 +1532,7 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
   for (int i = 0; st->master && i < st->n_tensors; ++i)
     if (st->master[i].data) add_span(spans, st->master[i], true, "master", i);
   add_moments(spans, st, eight, true);
-  if (st->d_t) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(st->d_t);
-    spans.push_back(Span{p, p + 16, 0, 0, false, true, "d_t", 0});
-  }
+  if (st->d_t) add_run(spans, st->d_t, 16, true, "d_t", 0);
   if ((s = check_overlap(spans)) != SMUON_OK) return s;
   if (plan && (s = check_ws(ws, ws_bytes, adamw_ws_bytes(st->n_tensors))) != SMUON_OK) return s;
   if ((s = device_info(&ex->di)) != SMUON_OK) return s;

@@ -218,6 +218,33 @@ def test_tensors_that_share_memory(L):
         assert call(*bad) == -1 and b"overlap" in L.smuon_last_error(), bad
 
 
+
+WIDE = dict(W=_m(0, cols=8, ld=16))  # rows of 32 bytes, 64 apart
+BETWEEN_ROWS = {  # what lies where, and whether it reaches from the gap behind a row into the next row
+    "d_t": (WIDE, dict(d_t=ADDR + 56), True),
+    "d_t in the gap": (WIDE, dict(d_t=ADDR + 40), False),
+    "scales": (dict(WIDE, **E8, scales=ADDR + 62), {}, False),  # one block: two bytes, the gap's last
+    "scales of two blocks": (dict(W=_m(0, rows=40, cols=8, ld=16), m=_m(1, rows=40, dt=S.E4M3), v=_m(2, rows=40, dt=S.E4M3),
+                                  scales=ADDR + 62), dict(rows=40), True),
+    "m": (dict(WIDE, m=S.SmuonMat(ADDR + 48, 4, 8, 8, S.F32)), {}, True),
+    "m in a wide gap": (dict(W=_m(0, cols=8, ld=80), m=S.SmuonMat(ADDR + 64, 4, 8, 8, S.F32)), {}, False),
+    "one row of m": (dict(WIDE, m=S.SmuonMat(ADDR + 48, 1, 32, 32, S.F32)), {}, True),
+}
+
+
+@pytest.mark.parametrize("name", list(BETWEEN_ROWS))
+def test_memory_between_the_rows_of_a_strided_weight(L, name):
+    """Whatever starts behind a row is refused where it reaches the next one, and taken where it does not."""
+    st_kw, more, meets = BETWEEN_ROWS[name]
+    st = _state(**st_kw, **{k: v for k, v in more.items() if k == "d_t"})
+    if not meets and torch.cuda.is_available():
+        pytest.skip("would run on made-up addresses")
+    code = L.adamw_step(ctypes.byref(st), _mats(_m(3, rows=more.get("rows", 4))), 1e-3, 0.9, 0.999, 1e-8, None, None, None, None)
+    if meets:
+        assert code == -1 and b"overlap" in L.smuon_last_error()
+    else:  # past every check of arguments: only the device is missing
+        assert code in (-6, -4) and b"overlap" not in L.smuon_last_error()
+
 def test_execute_refuses_other_plans(L):
     st = _state()
     assert L.adamw_execute(None, ctypes.byref(st), 1e-3, None) == -1
