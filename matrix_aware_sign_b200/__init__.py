@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+from contextlib import nullcontext
 from ctypes import POINTER, c_double, c_float, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 import torch
@@ -211,6 +212,11 @@ def _stream(stream):
     if stream is None:  # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us a call
         return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _torch_stream(handle, index):
+    """The stream of a handle on device `index` (handle 0 is the default stream; ExternalStream(0) would be a new one)."""
+    return torch.cuda.ExternalStream(handle, device=index) if handle else torch.cuda.default_stream(index)
 
 
 def workspace(nbytes: int, device=None) -> torch.Tensor:
@@ -636,8 +642,7 @@ class _Prepared:
         return s
 
     def _hold(self, s):
-        # (handle 0 is the default stream; ExternalStream(0) would be a new one)
-        stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream(self._index)
+        stream = _torch_stream(s, self._index)
         for t in self._own:  # allocated on the stream of the creation: not reused before this one is done with them
             t.record_stream(stream)
         self._seen.add(s)
@@ -729,8 +734,8 @@ class GradNorm(_Prepared):
 
 def smuon_grad_norm(G, max_norm: float, out, skip=None, ws=None, status=None, stream=None):
     """The norm of G into out (float32, two elements: norm, clip factor) and the
-    skip flag (int32), without a plan. Returns the workspace used: keep it until
-    the work on `stream` is done."""
+    skip flag (int32), without a plan. Returns the workspace used (a given one: keep
+    it until the work on `stream` is done)."""
     G = list(G)
     if out.dtype != torch.float32 or out.numel() != 2 or not out.is_contiguous():
         raise ValueError("out must be a contiguous float32 tensor of two elements")
@@ -738,7 +743,10 @@ def smuon_grad_norm(G, max_norm: float, out, skip=None, ws=None, status=None, st
     _scalar(status, torch.int32, "status")
     dev = _one_device(G, [out, skip, ws, status])
     if ws is None:
-        ws = workspace(smuon_grad_norm_workspace_bytes(G), dev)
+        n = smuon_grad_norm_workspace_bytes(G)
+        # from the memory of the stream that uses it: work queued on the current stream may still be using that stream's
+        with nullcontext() if stream is None else torch.cuda.stream(_torch_stream(_stream(stream), dev.index)):
+            ws = workspace(n, dev)
     with torch.cuda.device(dev):
         _check(lib().smuon_grad_norm(_tensors(G), len(G), max_norm, out.data_ptr(), _ptr(skip), ws.data_ptr(),
                                      ws.numel(), _ptr(status), _stream(stream)))

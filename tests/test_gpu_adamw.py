@@ -835,6 +835,23 @@ def test_norm_is_the_same_every_time():
     assert torch.equal(out, first)
 
 
+def test_norm_on_another_stream_takes_its_workspace_there():
+    """The workspace that the call makes for itself comes from the memory of the stream it runs on."""
+    G = [torch.randn(3000, device="cuda")]
+    out, side = torch.zeros(2, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream, handle in ((side, side.cuda_stream), (side.cuda_stream, side.cuda_stream), (None, 0)):
+        ws = S.smuon_grad_norm(G, 1.0, out, stream=stream)
+        torch.cuda.synchronize()
+        of = [seg["stream"] for seg in torch.cuda.memory_snapshot()
+              if seg["address"] <= ws.data_ptr() < seg["address"] + seg["total_size"]]
+        assert of == [handle]
+        want, _ = A.grad_norm([f64(G[0])], 1.0)
+        assert abs(float(out[0]) - want) <= 6 * U * want
+        out.zero_()
+        torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ a run of them together
 @pytest.mark.parametrize("eight", [False, True])
 def test_training_steps_beside_sign_muon(eight):
