@@ -518,8 +518,9 @@ typedef struct {
 } adamw_state;
 
 /* One step. lr, beta1, beta2 and eps are doubles because 1 - beta2 and the bias corrections need their digits.
- *  G[n]          gradients, F32 or BF16, shapes of W. Several entries may share memory; none may overlap a written
- *                tensor, and no two written tensors may overlap (SMUON_ERR_INVALID_ARG).
+ *  G[n]          gradients, F32 or BF16, shapes of W. Several entries may share memory; none of them, nor d_lr,
+ *                d_grad_scale or d_skip_if, may overlap a written tensor (d_t and scales are written, too), and
+ *                no two written tensors may overlap (SMUON_ERR_INVALID_ARG).
  *  lr            learning rate >= 0 (ignored with d_lr: device float, read when the step runs)
  *  beta1, beta2  in [0, 1);  eps > 0
  *  d_grad_scale  nullable device float: s (d_out + 1 of smuon_grad_norm)

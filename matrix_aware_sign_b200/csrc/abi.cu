@@ -1526,13 +1526,16 @@ smuon_status prepare_adamw(const adamw_state* st, const smuon_mat* G, double bet
                      (G[i].dtype == SMUON_BF16 ? AD_G_BF16 : 0) | (eight ? AD_8BIT : 0);
     by_kind[kind].push_back(T);
   }
-  spans.reserve(7 * (size_t)st->n_tensors + 1);
+  spans.reserve(7 * (size_t)st->n_tensors + 4);
   add_spans(spans, st->W, st->n_tensors, true, "W");
   add_spans(spans, G, st->n_tensors, false, "G");
   for (int i = 0; st->master && i < st->n_tensors; ++i)
     if (st->master[i].data) add_span(spans, st->master[i], true, "master", i);
   add_moments(spans, st, eight, true);
   if (st->d_t) add_run(spans, st->d_t, 16, true, "d_t", 0);
+  if (d_lr) add_run(spans, d_lr, 4, false, "d_lr", 0);
+  if (d_grad_scale) add_run(spans, d_grad_scale, 4, false, "d_grad_scale", 0);
+  if (d_skip_if) add_run(spans, d_skip_if, 4, false, "d_skip_if", 0);
   if ((s = check_overlap(spans)) != SMUON_OK) return s;
   if (plan && (s = check_ws(ws, ws_bytes, adamw_ws_bytes(st->n_tensors))) != SMUON_OK) return s;
   if ((s = device_info(&ex->di)) != SMUON_OK) return s;

@@ -245,6 +245,16 @@ def test_memory_between_the_rows_of_a_strided_weight(L, name):
     else:  # past every check of arguments: only the device is missing
         assert code in (-6, -4) and b"overlap" not in L.smuon_last_error()
 
+
+@pytest.mark.parametrize("which", ["d_lr", "d_grad_scale", "d_skip_if"])
+@pytest.mark.parametrize("at", [ADDR + 4, ADDR * 2 + 124, ADDR * 3, ADDR * 9, ADDR * 10 + 12])
+def test_scalars_in_written_memory(L, which, at):
+    """Every CTA reads them while others write: refused in W, m, v, scales and the device count."""
+    st = _state(**E8, scales=ADDR * 9, d_t=ADDR * 10) if at >= ADDR * 9 else _state()
+    d = {k: (at if k == which else None) for k in ("d_lr", "d_grad_scale", "d_skip_if")}
+    assert L.adamw_step(ctypes.byref(st), _mats(_m(3)), 1e-3, 0.9, 0.999, 1e-8, *d.values(), None) == -1
+    assert which.encode() in L.smuon_last_error() and b"overlap" in L.smuon_last_error()
+
 def test_execute_refuses_other_plans(L):
     st = _state()
     assert L.adamw_execute(None, ctypes.byref(st), 1e-3, None) == -1
