@@ -705,6 +705,7 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
     om[k >> 2] = k & 2 ? __byte_perm(om[k >> 2], a, 0x5410) : a;
     orr[k >> 2] = k & 2 ? __byte_perm(orr[k >> 2], b, 0x5410) : b;
   }
+  if (bm == 0) om[0] = om[1] = om[2] = om[3] = 0;  // held as zeros: no signs either
   if (__any_sync(0xffffffffu, near == 0u)) {
 #pragma unroll
     for (int k = 0; k < 16; k += 8) {

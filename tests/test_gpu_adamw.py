@@ -384,6 +384,26 @@ def test_extreme_gradients(eight):
         ref.check(opt, 0, w, tol + 2.0 ** -140)
 
 
+@pytest.mark.parametrize("odd", [0, 1])
+def test_moments_too_small_to_be_held_have_no_signs(odd):
+    """A block of first moments below 2^-119 is held as code 0 (not 0x80) for negative ones, too, at any address."""
+    n = 4 * 256 + 5
+    g = np.zeros(n)
+    g[[3, 300, n - 1]] = -1e-38
+    g[700:] = 0.01
+    g[701] = -1e-30  # and one whose block is held: code 0x80, its sign
+    g = A.f32(g)
+    buf = [torch.zeros(n + 1, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    m, v = (b[odd:odd + n].view(torch.float8_e4m3fn) for b in buf)
+    opt = S.AdamW([torch.zeros(n, device="cuda")], m=[m], v=[v], seed=1,
+                  scales=[torch.zeros(-(-n // 256), 2, dtype=torch.uint8, device="cuda")])
+    ref = Reference(np.zeros(n), np.zeros(n), np.zeros(n), True, 0, 1, wd=0.0)
+    S.adamw_step(opt, [dev(g.astype(np.float32))], LR, B1, B2, EPS)
+    w, tol = ref.step(g, 1)
+    assert not ref.cm[:512].any() and ref.cm[701] == 0x80
+    ref.check(opt, 0, w, tol + 2.0 ** -140)
+
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_non_finite_gradients_stay_where_they_are(eight):
     """A NaN or an infinity spoils its own weight and moments (8 bits: the moments of its block) and nothing else."""
