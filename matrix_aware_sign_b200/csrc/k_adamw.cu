@@ -670,7 +670,8 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   const float tm = half_warp_max(m, upper), tv = half_warp_max(v, upper);
   // finite, and so large (or zero) that the smallest v' which the root does not flush to zero is far below the codes
   if (!__all_sync(0xffffffffu, tm <= 0x1p120f && tv <= 0x1p120f && (tv == 0.f || tv >= 0x1p-80f))) return false;
-  if (c.eps < 0x1p-41f) {  // a root flushed to zero (below 2^-63) would show beside such an eps
+  // A root flushed to zero (below 2^-63) leaves out up to 2^-63 ic2 of a denominator of at least eps: 2^-24 of it, unless
+  if (c.eps < 0x1p-39f * c.ic2) {
     bool tiny = false;
 #pragma unroll
     for (int k = 0; k < 16; ++k) tiny |= v[k] > 0.f && v[k] < 0x1p-126f;

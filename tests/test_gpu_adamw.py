@@ -276,6 +276,25 @@ def test_small_eps_and_small_gradients(size, betas, eps):
     assert np.all(np.abs(f64(opt.W[0]) - w) <= U * (2 * np.abs(w) + 20 * LR * np.abs(u)))
 
 
+@pytest.mark.parametrize("b2", [0.999, 0.999999])
+@pytest.mark.parametrize("eps", [1e-12, 1e-10, 1e-9, 1e-8])
+def test_small_roots_beside_eps(eps, b2):
+    """Gradients near 2^-59 in the tiles of ordinary ones: their second moments are subnormal, and the bias correction
+    (32 and 1000 times the root in the first step) lifts the root towards eps. W starts at 0, so the step is all it holds."""
+    n = 2048
+    rng = np.random.default_rng(4)
+    g = rng.standard_normal(n) * 1e-3
+    g[::7] = np.exp2(rng.uniform(-62, -57, g[::7].size)) * rng.choice([-1.0, 1.0], g[::7].size)
+    g = A.f32(g)
+    opt = S.AdamW([torch.zeros(n, device="cuda")], bits=8, seed=2)
+    S.adamw_step(opt, [dev(g.astype(np.float32))], LR, B1, b2, eps)
+    m, v, r = A.moments(np.zeros(n), np.zeros(n), g, B1, b2)
+    assert np.any((v > 0) & (v < 2.0 ** -126))
+    u = A.direction(m, r, 1, B1, b2, eps)
+    w = -LR * u
+    assert np.all(np.abs(f64(opt.W[0]) - w) <= U * (2 * np.abs(w) + 20 * LR * np.abs(u)))
+
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_two_weights_in_one_matrix(eight):
     """Column halves of one matrix as two weights of a call."""
