@@ -488,11 +488,14 @@ smuon_status lionmuon_step(lionmuon_state* st, int32_t P, float beta1, float bet
  * of zeros (largest magnitude below 2^-119), 255 for a block that holds a NaN
  * or an infinity. A value is code * 2^(byte - 127) (0, respectively NaN, in
  * the last two cases); so zero bytes everywhere are zero moments. m' and r'
- * are rounded stochastically: with y = x * 2^(127 - byte), 16 random bits are
- * added at bit 4 of y's float32 pattern, the pattern is cut to three mantissa
- * bits and the result converted to E4M3 (to nearest, below 2^-6 the codes are
- * 2^-9 apart). Rounding to nearest would lose nearly every change of v: with
- * b2 = 0.999 its root moves by 0.05% in a step, a code step is 6 to 12%. The
+ * are rounded stochastically, each to one of its two neighbouring codes with
+ * the value as the mean: with z = x * 2^(7 - byte) (y = x * 2^(127 - byte) is
+ * what the codes stand for; z = y * 2^-120 is subnormal in float32, rounded to
+ * nearest even there, where y is below 2^-6 and the codes are 2^-9 apart), 16
+ * random bits are added at bit 4 of z's float32 pattern, and the code is its
+ * sign bit and bits 20 to 26. Rounding to nearest would lose nearly every
+ * change of v: with b2 = 0.999 its root moves by 0.05% in a step, a code step
+ * is 6 to 12%, and as large as the value itself at the smallest codes. The
  * random bits of entry e of tensor i (one number for both moments) are half
  * e % 2 of word (e % 8) / 2 of Philox4x32-10 at counter (e / 8 low word, e / 8
  * high word, low word of t, 1), key (seed, i): a run is a function of its inputs

@@ -198,25 +198,30 @@ __device__ __forceinline__ uint32_t block_exponent(const float (&x)[8]) {
   return top == 255u ? 255u : (top > 7u ? top - 7u : 0u);
 }
 
-// Codes of eight values. kRandom: 16 random bits added below the three mantissa bits that a code keeps,
-// then cut there (halves of rnd[4], low first), so that a code's mean is the value: the moments move by
-// far less than a code step (a second moment with b2 = 0.999 by 0.05% a step, a code step is 6 to 12%),
-// which rounding to nearest would lose every time. Else to nearest.
+// Codes of eight values. kRandom: a code goes up with the probability of its remainder, so that its mean is the value: the
+// moments move by far less than a code step (a second moment with b2 = 0.999 by 0.05% a step, a code step is 6 to 12%, and
+// as much as the value itself at the smallest codes), which rounding to nearest would lose every time. The values are
+// brought to 2^-120 times what the codes stand for, where float32's subnormal numbers begin with the codes' (below 2^-6,
+// 2^-9 apart): a pattern's sign bit and bits 20 to 26 are then the code at every size, and 16 random bits (halves of
+// rnd[4], low first) added at bit 4 carry into it. Else to nearest.
 template <bool kRandom>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte, const uint4 rnd) {
   if (byte == 0u || byte == 255u) return make_uint2(0u, 0u);
   const float up = __uint_as_float((254u - byte) << 23);
   const uint32_t rw[4] = {rnd.x, rnd.y, rnd.z, rnd.w};
-  uint32_t out[2];
+  uint32_t out[2] = {0u, 0u};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float2 y = make_float2(x[2 * k] * up, x[2 * k + 1] * up);
+  for (int k = 0; k < 8; k += 2) {
+    const float2 y = make_float2(x[k] * up, x[k + 1] * up);
+    uint32_t two;
     if (kRandom) {
-      y.x = __uint_as_float((__float_as_uint(y.x) + ((rw[k] & 0xffffu) << 4)) & 0xfff00000u);
-      y.y = __uint_as_float((__float_as_uint(y.y) + ((rw[k] >> 16) << 4)) & 0xfff00000u);
+      const uint32_t a = __float_as_uint(y.x * 0x1p-120f) + ((rw[k >> 1] & 0xffffu) << 4);
+      const uint32_t b = __float_as_uint(y.y * 0x1p-120f) + ((rw[k >> 1] >> 16) << 4);
+      two = (a >> 24 & 0x80u) | (a >> 20 & 0x7fu) | (b >> 16 & 0x8000u) | (b >> 12 & 0x7f00u);
+    } else {
+      two = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
     }
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-    out[k >> 1] = (k & 1) ? (out[k >> 1] | two << 16) : two;
+    out[k >> 2] |= two << (8 * (k & 2));
   }
   return make_uint2(out[0], out[1]);
 }
@@ -463,17 +468,18 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // a + b as a 1 + b, with a one that the assembler does not know to be one: it contracts mul.rn.f32x2 and add.rn.f32x2
 // into a single rounding (with -fmad=false, too), and the moments need both
 __device__ __forceinline__ F2 add2(F2 a, F2 b, float2 one) { return fma2(a, two(one.x, one.y), b); }
-// two codes (in the low half) to their values without scale; two float32 patterns to two codes in the low half
+// two codes (in the low half) to their values without scale
 __device__ __forceinline__ F2 values_of(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return two(f.x, f.y);
 }
-__device__ __forceinline__ uint32_t codes_of(uint32_t lo, uint32_t hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
-  return d;
+// codes of four entries from the patterns of encode8 with their random bits added; sign: a code's sign bits, where it has any
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&p)[4], uint32_t sign) {
+  constexpr uint32_t even = 0x00ff00ffu;  // entries 0 and 2 of the packed four
+  const uint32_t x = __byte_perm(p[0], p[2], 0x7632), y = __byte_perm(p[1], p[3], 0x7632);
+  return ((x >> 4) & even) | ((y << 4) & ~even) | ((((x >> 8) & even) | (y & ~even)) & sign);
 }
 
 // sixteen consecutive entries as loaded, and pairs of them as float32
@@ -634,9 +640,10 @@ __device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int
 //  - b1 m = (b1 2^k) code and b2 v = (b2 2^2k) code^2: a power of two commutes with the rounding, so the factor is
 //    formed once a block (while it is a normal number).
 //  - r' only goes into W' and into its code, which depends on r' through the carry out of its 20 low bits. An
-//    approximate root, made smaller by 2^-21 of itself, is below r' by less than 16 units in the last place and gives
-//    the same code unless those bits are within 16 of a carry: the warp then (one tile in 125) takes exact roots. The
-//    block's exponent comes from the exact root of the largest v' (rounding is monotonic).
+//    approximate root, made smaller by 2^-21 of itself, is below r' by less than 16 units in the last place (by fewer
+//    where the pattern is subnormal, whose units are wider) and gives the same code unless those bits are within 16 of a
+//    carry: the warp then (one tile in 125) takes exact roots. The block's exponent comes from the exact root of the
+//    largest v' (rounding is monotonic).
 // false where a value leaves the range in which this holds (nothing is written then).
 template <int kKind>
 __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane, const Consts& c, const AdHyper& h,
@@ -668,8 +675,9 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
     }
   }
   const float tm = half_warp_max(m, upper), tv = half_warp_max(v, upper);
-  // finite, and so large (or zero) that the smallest v' which the root does not flush to zero is far below the codes
-  if (!__all_sync(0xffffffffu, tm <= 0x1p120f && tv <= 0x1p120f && (tv == 0.f || tv >= 0x1p-80f))) return false;
+  // Finite, within what one factor brings to the codes' patterns (2^(7 - byte), a normal number), and so large (or zero)
+  // that a root flushed to zero (below 2^-63) is less than half a subnormal unit there.
+  if (!__all_sync(0xffffffffu, tm <= 0x1p13f && tv <= 0x1p24f && (tv == 0.f || tv >= 0x1p-50f))) return false;
   // A root flushed to zero (below 2^-63) leaves out up to 2^-63 ic2 of a denominator of at least eps: 2^-24 of it, unless
   if (c.eps < 0x1p-39f * c.ic2) {
     bool tiny = false;
@@ -679,8 +687,9 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   }
   const uint32_t fm = __float_as_uint(tm) >> 23, fr = __float_as_uint(__fsqrt_rn(tv)) >> 23;
   const uint32_t bm = fm > 7u ? fm - 7u : 0u, br = fr > 7u ? fr - 7u : 0u;
-  const F2 um = both(bm ? __uint_as_float((254u - bm) << 23) : 0.f);
-  const F2 ur = both(br ? __uint_as_float(((254u - br) << 23) - 8u) : 0.f);  // (1 - 2^-21) 2^j
+  const F2 um = both(bm ? __uint_as_float((134u - bm) << 23) : 0.f);
+  const F2 ur = both(br ? __uint_as_float(((134u - br) << 23) - 8u) : 0.f);  // (1 - 2^-21) 2^(7 - br)
+  const uint32_t sign = bm ? 0x80808080u : 0u;  // a block held as zeros has no signs
   const uint64_t grp = (uint64_t)e0 >> 3;
   const uint4 ra = group_words(grp, c.t, h.k0, T.id), rb = group_words(grp + 1, c.t, h.k0, T.id);
   const uint32_t rw[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
@@ -690,23 +699,28 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   w.from(stage + L::w + at * (int)sizeof(typename L::ST));
   uint32_t om[4], orr[4], near = 0xffffffffu;
 #pragma unroll
-  for (int k = 0; k < 16; k += 2) {
-    const F2 m2 = two(m[k], m[k + 1]), r2 = two(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), w2 = w.pair(k);
-    float d0, d1, a0, a1, b0, b1;
-    split(fma2(r2, ic2, eps), d0, d1);
-    split(fma2(step, mul2(m2, two(rcp_approx(d0), rcp_approx(d1))), fma2(decay, w2, w2)), a0, a1);
-    w.put(k, a0, a1);
-    split(mul2(m2, um), a0, a1);
-    split(mul2(r2, ur), b0, b1);
-    const uint32_t h0 = __byte_perm(rw[k >> 1], 0, 0x4410), h1 = __byte_perm(rw[k >> 1], 0, 0x4432);
-    const uint32_t pa0 = h0 * 16u + __float_as_uint(a0), pa1 = h1 * 16u + __float_as_uint(a1);
-    const uint32_t pb0 = h0 * 16u + __float_as_uint(b0), pb1 = h1 * 16u + __float_as_uint(b1);
-    near = min(near, min(~pb0 & 0xffff0u, ~pb1 & 0xffff0u));
-    const uint32_t a = codes_of(pa0 & 0xfff00000u, pa1 & 0xfff00000u), b = codes_of(pb0 & 0xfff00000u, pb1 & 0xfff00000u);
-    om[k >> 2] = k & 2 ? __byte_perm(om[k >> 2], a, 0x5410) : a;
-    orr[k >> 2] = k & 2 ? __byte_perm(orr[k >> 2], b, 0x5410) : b;
+  for (int k0 = 0; k0 < 16; k0 += 4) {
+    uint32_t pm[4], pr[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const int k = k0 + j;
+      const F2 m2 = two(m[k], m[k + 1]), r2 = two(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), w2 = w.pair(k);
+      float d0, d1, a0, a1, b0, b1;
+      split(fma2(r2, ic2, eps), d0, d1);
+      split(fma2(step, mul2(m2, two(rcp_approx(d0), rcp_approx(d1))), fma2(decay, w2, w2)), a0, a1);
+      w.put(k, a0, a1);
+      split(mul2(m2, um), a0, a1);
+      split(mul2(r2, ur), b0, b1);
+      const uint32_t h0 = __byte_perm(rw[k >> 1], 0, 0x4410), h1 = __byte_perm(rw[k >> 1], 0, 0x4432);
+      pm[j] = h0 * 16u + __float_as_uint(a0);
+      pm[j + 1] = h1 * 16u + __float_as_uint(a1);
+      pr[j] = h0 * 16u + __float_as_uint(b0);
+      pr[j + 1] = h1 * 16u + __float_as_uint(b1);
+      near = min(near, min(~pr[j] & 0xffff0u, ~pr[j + 1] & 0xffff0u));
+    }
+    om[k0 >> 2] = codes_of(pm, sign);
+    orr[k0 >> 2] = codes_of(pr, 0u);
   }
-  if (bm == 0) om[0] = om[1] = om[2] = om[3] = 0;  // held as zeros: no signs either
   if (__any_sync(0xffffffffu, near == 0u)) {
 #pragma unroll
     for (int k = 0; k < 16; k += 8) {

@@ -78,6 +78,16 @@ def _nearest_code(y):
     return (code | np.where(np.signbit(y), 128, 0)).astype(np.uint8)
 
 
+def _random_code(y, rnd):
+    """E4M3 code of each y (|y| < 256): the code below |y| or the next one, up where |y|'s place between the two (in 2^20
+    parts, and |y| < 2^-6 to multiples of 2^-29) and rnd / 2^16 together reach one."""
+    a = f32(np.abs(y) * 2.0 ** -120) * 2.0 ** 120
+    grid = np.exp2(np.maximum(np.frexp(a)[1] - 1, -6).astype(np.float64) - 3)
+    below = np.floor(a / grid)
+    up = a / grid - below + np.asarray(rnd, np.float64) * 2.0 ** -16 >= 1
+    return _nearest_code(np.copysign((below + up) * grid, y))
+
+
 def exponent_bytes(x):
     """Exponent byte of each block of a flat array of float32 values."""
     n = x.size
@@ -100,11 +110,8 @@ def encode(x, rnd=None):
     per = np.repeat(byte.astype(np.int64), BLOCK)[:x.size]
     live = (per > 0) & (per < 255)
     y = np.where(live, np.where(live, x, 0.0) * np.exp2(np.where(live, 127.0 - per, 0.0)), 0.0)
-    y = y.astype(np.float32)  # exact but for float32's own underflow
-    if rnd is not None:
-        bits = y.view(np.uint32) + (np.asarray(rnd, np.uint32) << np.uint32(4))
-        y = (bits & np.uint32(0xFFF00000)).view(np.float32)
-    return np.where(live, _nearest_code(y.astype(np.float64)), 0).astype(np.uint8), byte
+    code = _nearest_code(y) if rnd is None else _random_code(y, rnd)
+    return np.where(live, code, 0).astype(np.uint8), byte
 
 
 def decode(codes, byte):

@@ -113,6 +113,50 @@ def test_random_rounding_has_the_value_as_its_mean():
         assert abs(np.mean(got) - float(np.float32(x))) <= 2.0 ** -16 * step * 1.001
 
 
+def test_random_rounding_has_the_value_as_its_mean_at_every_size():
+    """The same down to 2^-17 of the block's largest, where codes are 2^-9 units apart (a unit: 1 / 128 to 1 / 256 of the
+    block's largest; here 1 / 192): off by less than 2^-16 of a code step, as above, and by the rounding to 2^-29 units."""
+    rnd = np.arange(65536, dtype=np.uint32)
+    unit = 2.0 ** -7
+    for x in [1.5 * 1.37 * 2.0 ** -k for k in range(1, 18)] + [-1.1e-4, 3.3 * 2.0 ** -16, 2.0 ** -17]:
+        got = []
+        for first in range(0, 65536, 255):
+            r = rnd[first:first + 255]
+            block = np.full(256, 1.5)
+            block[1:1 + r.size] = x
+            bits = np.zeros(256, np.uint32)
+            bits[1:1 + r.size] = r
+            c, b = A.encode(A.f32(block), bits)
+            assert b[0] == 120
+            got.append(A.decode(c, b)[1:1 + r.size])
+        got = np.concatenate(got)
+        step = max(2.0 ** (math.frexp(abs(x))[1] - 4), 2.0 ** -9 * unit)
+        assert abs(np.mean(got) - float(np.float32(x))) <= 2.0 ** -16 * step * 1.001 + 2.0 ** -30 * unit, x
+        assert np.ptp(got) == (step if len(set(got)) > 1 else 0) and np.all(np.abs(got - x) <= step)
+
+
+def test_moments_in_8_bits_decay_as_they_would_in_float32():
+    """255 entries whose gradients have ceased, beside one whose moments stay: over 400 steps the mean root falls by
+    b2^200, the mean first moment to nothing, at every size down to the smallest codes. The rounding leaves a mean
+    alone. A root that was a code of at most 16 steps moves by f <= 16 (1 - sqrt(b2)) = 0.008 steps and is rounded with
+    variance f (1 - f), so after 400 roundings the mean of 255 is within six times sqrt(400 * 0.008 / 255) = 0.67 code
+    steps (2^-9 units, or 2^-3 of the value at most) of its expectation."""
+    rng = np.random.default_rng(5)
+    b1, b2, steps = 0.9, 0.999, 400
+    for k in (3, 9, 12, 13, 14, 15):
+        x = np.full(256, 1.5)
+        x[1:] = 1.9 * 1.5 * 2.0 ** -k
+        m, r = x.copy(), x.copy()
+        for _ in range(steps):
+            noise = rng.integers(0, 65536, 256)
+            m, r = A.f32(b1 * m), A.f32(np.sqrt(b2) * r)
+            m[0] = r[0] = 1.5
+            m, r = A.decode(*A.encode(m, noise)), A.decode(*A.encode(r, noise))
+        step = max(2.0 ** -3 * x[1], 2.0 ** -9 * 2.0 ** -7)
+        assert abs(r[1:].mean() - x[1] * b2 ** (steps / 2)) <= 6 * math.sqrt(steps * 0.008 / 255) * step, k
+        assert np.abs(m[1:]).mean() <= x[1] * b1 ** steps + 2.0 ** -9 * 2.0 ** -7, k
+
+
 def test_rounding_bits_come_from_the_repositorys_generator():
     """Word i of the Philox block of group e / 8 serves entries 2i (low half) and 2i + 1 (high half)."""
     got = A.rounding_bits(40, 6, 11, 5)

@@ -404,6 +404,29 @@ def test_extreme_gradients(eight):
 
 
 @pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("size", [2.0 ** -44, 1e-9, 1e-3, 1.0, 7e4, 1e7, 1e15])
+def test_small_codes_beside_large_ones(size, odd):
+    """Blocks whose moments span all that a block can hold (2^16) and more, codes of every size: of 4 steps, the later ones
+    without gradients but for the blocks' largest. Sizes on either side of what the form for whole tiles takes."""
+    n = 8 * 256 + 77
+    rng = np.random.default_rng(6)
+    g = A.f32(size * rng.choice([-1.0, 1.0], n) * np.exp2(rng.uniform(-26, 0, n)))
+    g[::256] = A.f32(size)
+    only = np.where(np.arange(n) % 256 == 0, g, 0.0)
+    buf = [torch.zeros(n + 1, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    m, v = (b[odd:odd + n].view(torch.float8_e4m3fn) for b in buf)
+    opt = S.AdamW([torch.zeros(n, device="cuda")], m=[m], v=[v], seed=8,
+                  scales=[torch.zeros(-(-n // 256), 2, dtype=torch.uint8, device="cuda")])
+    ref = Reference(np.zeros(n), np.zeros(n), np.zeros(n), True, 0, 8, wd=0.0)
+    for t in range(1, 5):
+        S.adamw_step(opt, [dev((g if t == 1 else only).astype(np.float32))], LR, B1, B2, EPS)
+        w, tol = ref.step(g if t == 1 else only, t)
+        ref.check(opt, 0, w, tol + 2.0 ** -140)
+        small = (ref.cr & 127) < 8
+        assert small.any() and (ref.cm[small] != 0).any()
+
+
+@pytest.mark.parametrize("odd", [0, 1])
 def test_moments_too_small_to_be_held_have_no_signs(odd):
     """A block of first moments below 2^-119 is held as code 0 (not 0x80) for negative ones, too, at any address."""
     n = 4 * 256 + 5
