@@ -495,7 +495,11 @@ smuon_status lionmuon_step(lionmuon_state* st, int32_t P, float beta1, float bet
  * random bits are added at bit 4 of z's float32 pattern, and the code is its
  * sign bit and bits 20 to 26. Rounding to nearest would lose nearly every
  * change of v: with b2 = 0.999 its root moves by 0.05% in a step, a code step
- * is 6 to 12%, and as large as the value itself at the smallest codes. The
+ * is 6 to 12%, and as large as the value itself at the smallest codes. An
+ * r' that is not zero gets at least the smallest code, 2^-9, in a block that
+ * is held (a root cut to zero beside a first moment that is not would leave
+ * eps alone as that moment's denominator), so where an entry's root is below
+ * 2^-16 of its block's largest, its steps are smaller than with F32 moments. The
  * random bits of entry e of tensor i (one number for both moments) are half
  * e % 2 of word (e % 8) / 2 of Philox4x32-10 at counter (e / 8 low word, e / 8
  * high word, low word of t, 1), key (seed, i): a run is a function of its inputs
@@ -546,7 +550,7 @@ smuon_status adamw_execute(smuon_plan plan, adamw_state* st, double lr, void* st
 
 /* dst's moments <- src's moments, from F32 to SMUON_E4M3 or back (the other direction of types, or two states of one
  * type, are SMUON_ERR_DTYPE; tensor i of both must have the same number of entries). To 8 bits values are rounded to
- * nearest even code. dst->t <- src->t; with device counts (both states have one, or neither) the count is copied on
+ * nearest even code (roots that are not zero to at least the smallest). dst->t <- src->t; with device counts (both states have one, or neither) the count is copied on
  * the stream. Weights are not touched. */
 smuon_status adamw_convert(const adamw_state* src, adamw_state* dst, void* stream);
 

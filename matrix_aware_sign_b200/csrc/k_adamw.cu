@@ -198,13 +198,25 @@ __device__ __forceinline__ uint32_t block_exponent(const float (&x)[8]) {
   return top == 255u ? 255u : (top > 7u ? top - 7u : 0u);
 }
 
+// A root that is not zero keeps at least the smallest code. Cut to zero beside a first moment that is held, it would leave
+// eps alone under that moment: a step of a thousand learning rates where a gradient is 1e-5 of its block's largest. x:
+// the roots, or their squares; few lanes have a code of zero to look at (zero_codes).
+template <int N>
+__device__ __forceinline__ void keep_roots(const float (&x)[N], uint32_t (&codes)[N / 4]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (x[k] > 0.f && !(codes[k >> 2] & 0x7fu << (8 * (k & 3)))) codes[k >> 2] |= 1u << (8 * (k & 3));
+}
+// high bits where one of four codes (none of them negative) is zero, or stands behind one that is
+__device__ __forceinline__ uint32_t zero_codes(uint32_t codes) { return codes - 0x01010101u; }
+
 // Codes of eight values. kRandom: a code goes up with the probability of its remainder, so that its mean is the value: the
 // moments move by far less than a code step (a second moment with b2 = 0.999 by 0.05% a step, a code step is 6 to 12%, and
 // as much as the value itself at the smallest codes), which rounding to nearest would lose every time. The values are
 // brought to 2^-120 times what the codes stand for, where float32's subnormal numbers begin with the codes' (below 2^-6,
 // 2^-9 apart): a pattern's sign bit and bits 20 to 26 are then the code at every size, and 16 random bits (halves of
 // rnd[4], low first) added at bit 4 carry into it. Else to nearest.
-template <bool kRandom>
+template <bool kRandom, bool kRoot>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte, const uint4 rnd) {
   if (byte == 0u || byte == 255u) return make_uint2(0u, 0u);
   const float up = __uint_as_float((254u - byte) << 23);
@@ -223,6 +235,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte, con
     }
     out[k >> 2] |= two << (8 * (k & 2));
   }
+  if (kRoot && ((zero_codes(out[0]) | zero_codes(out[1])) & 0x80808080u)) keep_roots(x, out);
   return make_uint2(out[0], out[1]);
 }
 
@@ -409,8 +422,8 @@ __device__ __noinline__ void step_block8(const AdTensor& T, int64_t blk, int lan
   const uint32_t bm = block_exponent(m), br = block_exponent(r);
   const uint64_t grp = (uint64_t)first >> 3;
   const uint4 rnd = crng::philox4x32_10(make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), c.t, 1u), c.seed, T.id);
-  store_codes(reinterpret_cast<uint8_t*>(T.m), first, n, false, encode8<true>(m, bm, rnd));
-  store_codes(reinterpret_cast<uint8_t*>(T.v), first, n, false, encode8<true>(r, br, rnd));
+  store_codes(reinterpret_cast<uint8_t*>(T.m), first, n, false, encode8<true, false>(m, bm, rnd));
+  store_codes(reinterpret_cast<uint8_t*>(T.v), first, n, false, encode8<true, true>(r, br, rnd));
   if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
 }
 
@@ -676,8 +689,9 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   }
   const float tm = half_warp_max(m, upper), tv = half_warp_max(v, upper);
   // Finite, within what one factor brings to the codes' patterns (2^(7 - byte), a normal number), and so large (or zero)
-  // that a root flushed to zero (below 2^-63) is less than half a subnormal unit there.
-  if (!__all_sync(0xffffffffu, tm <= 0x1p13f && tv <= 0x1p24f && (tv == 0.f || tv >= 0x1p-50f))) return false;
+  // that a root flushed to zero (below 2^-63) is far below the codes: its random bits bring it to the smallest at most,
+  // which it gets in any case.
+  if (!__all_sync(0xffffffffu, tm <= 0x1p13f && tv <= 0x1p24f && (tv == 0.f || tv >= 0x1p-80f))) return false;
   // A root flushed to zero (below 2^-63) leaves out up to 2^-63 ic2 of a denominator of at least eps: 2^-24 of it, unless
   if (c.eps < 0x1p-39f * c.ic2) {
     bool tiny = false;
@@ -697,7 +711,7 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   const F2 step = both(-lr * c.ic1), decay = both(-lr * T.wd), ic2 = both(c.ic2), eps = two(h.eps2.x, h.eps2.y);
   Raw16<typename L::ST> w;
   w.from(stage + L::w + at * (int)sizeof(typename L::ST));
-  uint32_t om[4], orr[4], near = 0xffffffffu;
+  uint32_t om[4], orr[4], near = 0xffffffffu, zero = 0;
 #pragma unroll
   for (int k0 = 0; k0 < 16; k0 += 4) {
     uint32_t pm[4], pr[4];
@@ -720,6 +734,7 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
     }
     om[k0 >> 2] = codes_of(pm, sign);
     orr[k0 >> 2] = codes_of(pr, 0u);
+    zero |= zero_codes(orr[k0 >> 2]);
   }
   if (__any_sync(0xffffffffu, near == 0u)) {
 #pragma unroll
@@ -727,11 +742,12 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
       float r[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[j] = __fsqrt_rn(v[k + j]);
-      const uint2 x = encode8<true>(r, br, k ? rb : ra);
+      const uint2 x = encode8<true, true>(r, br, k ? rb : ra);
       orr[k >> 2] = x.x;
       orr[(k >> 2) + 1] = x.y;
     }
   }
+  if (br && (zero & 0x80808080u)) keep_roots(v, orr);
   if (!(T.flags & kAdVecW)) {  // W off its vector addresses: through the stage, entry by entry
     __syncwarp();  // its own copy has been read
     WT* const out = reinterpret_cast<WT*>(stage + L::w);
@@ -1147,8 +1163,8 @@ __device__ __forceinline__ void convert_to8(const ConvTensor& T, int64_t blk, in
 #pragma unroll
   for (int k = 0; k < 8; ++k) r[k] = __fsqrt_rn(r[k]);
   const uint32_t bm = block_exponent(m), br = block_exponent(r);
-  store_codes(reinterpret_cast<uint8_t*>(T.m8), e0, T.n, vec, encode8<false>(m, bm, make_uint4(0, 0, 0, 0)));
-  store_codes(reinterpret_cast<uint8_t*>(T.v8), e0, T.n, vec, encode8<false>(r, br, make_uint4(0, 0, 0, 0)));
+  store_codes(reinterpret_cast<uint8_t*>(T.m8), e0, T.n, vec, encode8<false, false>(m, bm, make_uint4(0, 0, 0, 0)));
+  store_codes(reinterpret_cast<uint8_t*>(T.v8), e0, T.n, vec, encode8<false, true>(r, br, make_uint4(0, 0, 0, 0)));
   if (lane == 0) *reinterpret_cast<uint16_t*>(T.scales + 2 * blk) = (uint16_t)(bm | br << 8);
 }
 __device__ __forceinline__ void convert_to32(const ConvTensor& T, int64_t blk, int lane, uint32_t sc, uint2 cm, uint2 cr) {

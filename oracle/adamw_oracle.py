@@ -26,6 +26,10 @@ def f32(x):
         return np.asarray(x, np.float64).astype(np.float32).astype(np.float64)
 
 
+class Roots(np.ndarray):
+    """Second moments' roots: encode() keeps those that are not zero."""
+
+
 def moments(m, v, g, beta1, beta2, scale=None):
     """(m', v', r') of float32 moments and gradients, with the definition's float32 roundings."""
     b1, c1, b2, c2 = f32(beta1), f32(1 - beta1), f32(beta2), f32(1 - beta2)
@@ -35,7 +39,7 @@ def moments(m, v, g, beta1, beta2, scale=None):
             g = f32(f32(scale) * g)
         m = f32(f32(b1 * m) + f32(c1 * g))
         v = f32(f32(b2 * v) + f32(c2 * f32(g * g)))
-        return m, v, f32(np.sqrt(v))
+        return m, v, f32(np.sqrt(v)).view(Roots)
 
 
 def direction(m, r, t, beta1, beta2, eps):
@@ -104,13 +108,17 @@ def exponent_bytes(x):
 
 
 def encode(x, rnd=None):
-    """(codes, exponent bytes) of a flat array; rnd: 16 random bits per entry, None: to nearest."""
+    """(codes, exponent bytes) of a flat array; rnd: 16 random bits per entry, None: to nearest. Roots that are not zero
+    get at least the smallest code (in a block that is held)."""
+    least = isinstance(x, Roots)
     x = np.asarray(x, np.float64).reshape(-1)
     byte = exponent_bytes(x)
     per = np.repeat(byte.astype(np.int64), BLOCK)[:x.size]
     live = (per > 0) & (per < 255)
     y = np.where(live, np.where(live, x, 0.0) * np.exp2(np.where(live, 127.0 - per, 0.0)), 0.0)
     code = _nearest_code(y) if rnd is None else _random_code(y, rnd)
+    if least:
+        code = np.where(x > 0, np.maximum(code, 1), code)
     return np.where(live, code, 0).astype(np.uint8), byte
 
 

@@ -157,6 +157,37 @@ def test_moments_in_8_bits_decay_as_they_would_in_float32():
         assert np.abs(m[1:]).mean() <= x[1] * b1 ** steps + 2.0 ** -9 * 2.0 ** -7, k
 
 
+def test_roots_that_are_not_zero_stay():
+    """Whatever the random bits, and to nearest: a root below the smallest code gets it, zero stays zero, a block that is
+    too small to be held is held as zeros; first moments are rounded as they are."""
+    x = np.zeros(512)
+    x[:4] = 1.5, 1e-9, 0.0, 2.0 ** -17
+    x[256:] = 2.0 ** -120
+    _, _, r = A.moments(np.zeros(512), x * x, np.zeros(512), 0.5, 1 - 2.0 ** -30)
+    for rnd in (None, np.zeros(512, np.uint32), np.full(512, 65535, np.uint32)):
+        c, b = A.encode(r, rnd)
+        assert list(c[1:3]) == [1, 0] and c[3] >= 1 and not c[4:].any() and b[1] == 0
+        m, _ = A.encode(np.asarray(r), rnd)
+        # 1e-9 is 6.6e-5 of the smallest code's 2^-16 (a unit is 2^-7): the largest random number alone brings it there
+        assert m[1] == (rnd is not None and rnd[1] == 65535) and m[0] == c[0]
+
+
+def test_no_first_moment_is_held_over_a_root_of_zero():
+    """300 steps in 8 bits of entries whose gradients are 1e-5 of their block's largest: m' is not zero only where a gradient
+    was not, and there v' is not zero either, so no direction has eps alone for its denominator."""
+    rng = np.random.default_rng(2)
+    cm = cr = np.zeros(256, np.uint8)
+    bm = br = np.zeros(1, np.uint8)
+    for t in range(1, 301):
+        g = rng.standard_normal(256) * 1e-5
+        g[0] = rng.standard_normal()
+        m, r = A.decode(cm, bm), A.decode(cr, br)
+        m, v, r = A.moments(m, r * r, A.f32(g), 0.9, 0.999)
+        rnd = rng.integers(0, 65536, 256)
+        (cm, bm), (cr, br) = A.encode(m, rnd), A.encode(r, rnd)
+        assert not np.any(((cm & 127) > 0) & (cr == 0)), t
+
+
 def test_rounding_bits_come_from_the_repositorys_generator():
     """Word i of the Philox block of group e / 8 serves entries 2i (low half) and 2i + 1 (high half)."""
     got = A.rounding_bits(40, 6, 11, 5)

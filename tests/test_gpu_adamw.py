@@ -796,6 +796,21 @@ def test_convert_both_ways():
             assert np.all(np.abs(x - y)[small] <= 2.0 ** -10 * unit[small])
 
 
+@pytest.mark.parametrize("odd", [0, 1])
+def test_convert_keeps_roots_that_are_not_zero(odd):
+    n = 700
+    v = A.f32(np.exp2(np.random.default_rng(3).uniform(-60, 0, n)))
+    v[5] = 0.0
+    src = S.AdamW([torch.zeros(n, device="cuda")], m=[torch.ones(n, device="cuda")], v=[dev(v.astype(np.float32))])
+    buf = [torch.zeros(n + 1, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    m8, v8 = (b[odd:odd + n].view(torch.float8_e4m3fn) for b in buf)
+    dst = S.AdamW(src.W, m=[m8], v=[v8], scales=[torch.zeros(3, 2, dtype=torch.uint8, device="cuda")])
+    S.adamw_convert(src, dst)
+    c, b = A.encode(A.f32(np.sqrt(v)).view(A.Roots))
+    assert np.array_equal(bits(v8), c) and np.array_equal(dst.scales[0][:, 1].cpu().numpy(), b)
+    assert c[5] == 0 and (np.delete(c, 5) >= 1).all() and (c == 1).sum() > 100
+
+
 def test_convert_at_odd_addresses_and_counts():
     n = 777
     m, v = torch.randn(n + 3, device="cuda")[3:], torch.rand(n + 1, device="cuda")[1:]
