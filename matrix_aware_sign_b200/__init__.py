@@ -203,13 +203,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# the current device and a device's current stream as bare numbers (a CPU-only PyTorch has neither)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and a device's current stream as bare numbers, by PyTorch's own short ways where it has them
+# (torch.cuda.current_stream() builds a Stream object, 3 us a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream(stream):
-    if stream is None:  # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us a call
+    if stream is None:
         return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 

@@ -3,6 +3,7 @@
 counter generator), the rounding's mean, and the host checks of every entry
 point: bad arguments are refused before a device would be touched."""
 import ctypes
+import importlib.util
 import math
 from fractions import Fraction
 
@@ -465,3 +466,15 @@ def test_a_plan_asks_its_own_device_for_a_capture(monkeypatch):
     assert Device.current == 0
     with S._Prepared()._uploading(torch.device("cuda:0")):
         assert Device.current == 0
+
+
+def test_the_current_stream_without_pytorchs_short_ways(monkeypatch):
+    """On a PyTorch without these private names the public calls give the current stream's handle, to every operator."""
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: type("Stream", (), {"cuda_stream": 100 + index}))
+    spec = importlib.util.spec_from_file_location("binding_again", S.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert again._current_device() == 3 and again._stream(None) == 103 and again._stream(7) == 7
