@@ -747,6 +747,61 @@ def test_offsets_beyond_32_bits(eight):
     assert abs(float(norm.norm) - want) <= 6 * U * want
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_weights_beyond_32_bits_are_stepped(eight):
+    """A learning rate that moves bf16 weights by many of their steps: every place differs from where it was, at the start,
+    at the 2^31 border, in between and at the end."""
+    n = (1 << 31) + 1554
+    if torch.cuda.mem_get_info()[0] < (14 if eight else 27) * n // 2 + (2 << 30):
+        pytest.skip("needs more free memory")
+    W = torch.full((2, n // 2), 0.5, dtype=BF16, device="cuda")
+    G = torch.full((2, n // 2), 2.0 ** -9, dtype=BF16, device="cuda")
+    flat_w, flat_g = W.view(-1), G.view(-1)
+    places = [0, (1 << 30) + 512, (1 << 31) - 512, 1 << 31, (n // 256 - 1) * 256]
+    rng = np.random.default_rng(1)
+    for p in places:
+        size = min(512, n - p)
+        flat_g[p:p + size] = dev((rng.standard_normal(size) * 1e-2).astype(np.float32)).to(BF16)
+    opt = S.AdamW([W], bits=8 if eight else 32, weight_decay=WD, seed=6)
+    S.adamw_step(opt, [G], 0.25, B1, B2, EPS)
+    for p in places:
+        size = min(512, n - p)
+        g, z = f64(flat_g[p:p + size]), np.zeros(size)
+        m, _, r = A.moments(z, z, g, B1, B2)
+        u = A.direction(m, np.asarray(r), 1, B1, B2, EPS)
+        w = 0.5 - 0.25 * (WD * 0.5 + u)
+        got = f64(flat_w[p:p + size])
+        assert np.all(np.abs(got - w) <= 2.0 ** -8 * np.abs(w) + U * (2 * np.abs(w) + 20 * 0.25 * (np.abs(u) + WD * 0.5)))
+        assert np.all(np.abs(got - 0.5) > 0.1)
+    # all the others had one gradient (whose direction is 1 but for eps, 5e-6 of it)
+    w = 0.5 - 0.25 * (WD * 0.5 + 1)
+    for p in places:
+        flat_w[p:p + 512] = w
+    assert all(bool(((part.float() - w).abs() <= (2.0 ** -8 + 2.0 ** -14) * w).all()) for part in flat_w.split(1 << 28))
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("cols,ld,off", [(704, (1 << 30) + 16, 0), (701, (1 << 30) + 5, 3)])
+def test_rows_more_than_32_bits_apart(cols, ld, off, eight):
+    """W and G as three rows whose last begins beyond 2^31 entries, on vector addresses and off them; the norm of such
+    gradients; nothing else in W's buffer changes."""
+    total = 2 * ld + cols + off
+    if torch.cuda.mem_get_info()[0] < 6 * total:
+        pytest.skip("needs more free memory")
+    wbuf, gbuf = (torch.zeros(total, dtype=BF16, device="cuda") for _ in range(2))
+    W, G = (b.as_strided((3, cols), (ld, 1), off) for b in (wbuf, gbuf))
+    w, g, _, _ = draw_tensor(np.random.default_rng(3), (3, cols))
+    W.copy_(torch.from_numpy(w.astype(np.float32)).reshape(3, cols))
+    G.copy_(torch.from_numpy(g.astype(np.float32)).reshape(3, cols))
+    ref = Reference(f64(W.contiguous()), np.zeros(3 * cols), np.zeros(3 * cols), eight, 0, 6, bf16=True)
+    opt = S.AdamW([W], bits=8 if eight else 32, weight_decay=WD, seed=6)
+    check_norm([G], 1.0)
+    S.adamw_step(opt, [G], LR, B1, B2, EPS)
+    ref.check(opt, 0, *ref.step(f64(G.contiguous()), 1))
+    W.zero_()
+    assert not any(bool(part.any()) for part in wbuf.split(1 << 28))
+
+
 def test_results_do_not_depend_on_the_split():
     """The same tensors in one call, one by one in calls of their own (32 bits), and prepared: equal bits."""
     shapes = [(257,), (40, 41), (3000,)]
