@@ -688,10 +688,10 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
     }
   }
   const float tm = half_warp_max(m, upper), tv = half_warp_max(v, upper);
-  // Finite, within what one factor brings to the codes' patterns (2^(7 - byte), a normal number), and so large (or zero)
+  // Finite, within what one factor brings to the codes' patterns (2^(7 - byte), 2^-149 at least), and so large (or zero)
   // that a root flushed to zero (below 2^-63) is far below the codes: its random bits bring it to the smallest at most,
   // which it gets in any case.
-  if (!__all_sync(0xffffffffu, tm <= 0x1p13f && tv <= 0x1p24f && (tv == 0.f || tv >= 0x1p-80f))) return false;
+  if (!__all_sync(0xffffffffu, tm <= 0x1p36f && tv <= 0x1p72f && (tv == 0.f || tv >= 0x1p-80f))) return false;
   // A root flushed to zero (below 2^-63) leaves out up to 2^-63 ic2 of a denominator of at least eps: 2^-24 of it, unless
   if (c.eps < 0x1p-39f * c.ic2) {
     bool tiny = false;
@@ -701,14 +701,15 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
   }
   const uint32_t fm = __float_as_uint(tm) >> 23, fr = __float_as_uint(__fsqrt_rn(tv)) >> 23;
   const uint32_t bm = fm > 7u ? fm - 7u : 0u, br = fr > 7u ? fr - 7u : 0u;
-  const F2 um = both(bm ? __uint_as_float((134u - bm) << 23) : 0.f);
-  const F2 ur = both(br ? __uint_as_float(((134u - br) << 23) - 8u) : 0.f);  // (1 - 2^-21) 2^(7 - br)
+  const F2 um = both(bm ? __uint_as_float((158u - bm) << 23) * 0x1p-24f : 0.f);  // 2^(7 - byte), subnormal or not
+  const F2 ur = both(br ? __uint_as_float((158u - br) << 23) * 0x1p-24f : 0.f);
+  const F2 low = both(1.f - 0x1p-21f), ic2 = both(c.ic2 * (1.f + 0x1p-21f));  // the root that is made smaller, and its weight
   const uint32_t sign = bm ? 0x80808080u : 0u;  // a block held as zeros has no signs
   const uint64_t grp = (uint64_t)e0 >> 3;
   const uint4 ra = group_words(grp, c.t, h.k0, T.id), rb = group_words(grp + 1, c.t, h.k0, T.id);
   const uint32_t rw[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
   const float lr = c.lr * T.lr_scale;
-  const F2 step = both(-lr * c.ic1), decay = both(-lr * T.wd), ic2 = both(c.ic2), eps = two(h.eps2.x, h.eps2.y);
+  const F2 step = both(-lr * c.ic1), decay = both(-lr * T.wd), eps = two(h.eps2.x, h.eps2.y);
   Raw16<typename L::ST> w;
   w.from(stage + L::w + at * (int)sizeof(typename L::ST));
   uint32_t om[4], orr[4], near = 0xffffffffu, zero = 0;
@@ -718,7 +719,7 @@ __device__ __forceinline__ bool step_tile8(const AdTensor& T, int tile, int lane
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
       const int k = k0 + j;
-      const F2 m2 = two(m[k], m[k + 1]), r2 = two(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), w2 = w.pair(k);
+      const F2 m2 = two(m[k], m[k + 1]), r2 = mul2(two(sqrt_approx(v[k]), sqrt_approx(v[k + 1])), low), w2 = w.pair(k);
       float d0, d1, a0, a1, b0, b1;
       split(fma2(r2, ic2, eps), d0, d1);
       split(fma2(step, mul2(m2, two(rcp_approx(d0), rcp_approx(d1))), fma2(decay, w2, w2)), a0, a1);

@@ -426,6 +426,25 @@ def test_small_codes_beside_large_ones(size, odd):
         assert small.any() and (ref.cm[small] != 0).any()
 
 
+@pytest.mark.parametrize("small", [1.0, 2.0 ** -20, 2.0 ** -45, 2.0 ** -60, 2.0 ** -75, 1e-30, 0.0])
+@pytest.mark.parametrize("large", [2e4, 2e5, 1e9, 3e11, 1e13, 2.0 ** 62])
+def test_large_gradients_beside_small_ones(large, small):
+    """Tiles with moments beyond what a single factor brings to the codes' patterns, beside moments of any smaller size: in
+    the same block, and in the tile's other block. W starts at 0, so the step is all it holds."""
+    n = 4 * 512
+    rng = np.random.default_rng(7)
+    g = rng.standard_normal(n) * large
+    g[0:256:3] = rng.standard_normal(g[0:256:3].size) * small     # the same block
+    g[512 + 256:1024] = rng.standard_normal(256) * small          # the tile's other block
+    g = A.f32(g)
+    opt = S.AdamW([torch.zeros(n, device="cuda")], bits=8, seed=2)
+    ref = Reference(np.zeros(n), np.zeros(n), np.zeros(n), True, 0, 2, wd=0.0)
+    for t in (1, 2, 3):
+        S.adamw_step(opt, [dev(g.astype(np.float32))], LR, B1, B2, EPS)
+        w, tol = ref.step(g, t)
+        ref.check(opt, 0, w, tol + 2.0 ** -140)
+
+
 @pytest.mark.parametrize("odd", [0, 1])
 def test_moments_too_small_to_be_held_have_no_signs(odd):
     """A block of first moments below 2^-119 is held as code 0 (not 0x80) for negative ones, too, at any address."""
