@@ -919,11 +919,14 @@ namespace {
 template <int kKind, class Table>
 cudaError_t launch_kind(const Table& tb, const AdHyper& h, int sms, cudaStream_t s) {
   if constexpr (Kind<kKind>::eight) {
-    // As many CTAs as are resident, with equal stretches; from eight times what those do at 24 tiles a warp on, CTAs of
-    // 24 tiles a warp that follow one another, whose stretches stay close together in memory: 774M entries with master
-    // 2.32 -> 2.08 ms (82 to 91% of the copy rate), while 65.6M entries (2.3 rounds of such CTAs) go from 134 to 141 us.
+    // As many CTAs as are resident, with equal stretches; from four times what those do at 24 tiles a warp on (117M entries
+    // on 148 SMs), CTAs of 24 tiles a warp that follow one another, whose stretches stay close together in memory. Both
+    // forms on one box, us (resident / following), bf16 without a master: 33M entries 72 / 84, 66M 138 / 146, 90M 186 /
+    // 189, 118M 242 / 242, 131M 268 / 266, 233M 472 / 455, 774M 1,578 / 1,506; bf16 with a master: 33M 100 / 114, 66M 194 /
+    // 188, 118M 341 / 312, 233M 667 / 592, 774M 2,177 / 1,913; float32: 33M 101 / 112, 66M 199 / 183, 118M 341 / 309, 774M
+    // 2,116 / 1,866. What crosses is the round of CTAs that is left over at the end, so the latest type sets the border.
     const int want = (tb.total_tiles + kAd8Warps - 1) / kAd8Warps, resident = sms * kAd8Ctas;
-    const int grid = want < 1 ? 1 : want < resident ? want : want / kAd8Run >= 8 * resident ? want / kAd8Run : resident;
+    const int grid = want < 1 ? 1 : want < resident ? want : want / kAd8Run >= 4 * resident ? want / kAd8Run : resident;
     return launch(k_adamw8<kKind, Table>, grid, 32 * kAd8Warps, kAd8Warps * 2 * Stage<kKind>::bytes, s, tb, h);
   } else {
     const int want = (int)((2 * (int64_t)tb.total_tiles + kAd32Warps - 1) / kAd32Warps);
