@@ -33,7 +33,7 @@ def _put(dst: torch.Tensor, src: torch.Tensor, name: str) -> None:
     if dst.shape != src.shape or dst.dtype != src.dtype:
         raise ValueError(f"checkpoint entry {name}: {tuple(src.shape)} {src.dtype} does not fit "
                          f"{tuple(dst.shape)} {dst.dtype}")
-    dst.copy_(src.to(dst.device), non_blocking=False)
+    dst.detach().copy_(src.to(dst.device), non_blocking=False)  # parameters that require gradients, too
 
 
 def _tensors(obj):

@@ -32,3 +32,13 @@ def test_restore_refuses_a_different_run():
         C.restore({"W": torch.zeros(4, 4, dtype=torch.float64)}, snap)
     with pytest.raises(TypeError):
         C.snapshot([torch.zeros(1)])
+
+
+def test_restore_into_parameters():
+    """A model's parameters require gradients; restoring writes them in place all the same."""
+    state = {"W": torch.nn.Parameter(torch.ones(3, 4))}
+    snap = C.snapshot(state)
+    with torch.no_grad():
+        state["W"].add_(1)
+    C.restore(state, snap)
+    assert torch.equal(state["W"].detach(), torch.ones(3, 4)) and state["W"].requires_grad
