@@ -529,7 +529,7 @@ typedef struct {
  *                d_grad_scale or d_skip_if, may overlap a written tensor (d_t and scales are written, too), and
  *                no two written tensors may overlap (SMUON_ERR_INVALID_ARG).
  *  lr            learning rate >= 0 (ignored with d_lr: device float, read when the step runs)
- *  beta1, beta2  in [0, 1);  eps > 0
+ *  beta1, beta2  in [0, 1);  eps in 1e-30 .. 1e30
  *  d_grad_scale  nullable device float: s (d_out + 1 of smuon_grad_norm)
  *  d_skip_if     nullable device int32: when nonzero at run time the step leaves everything as it was
  * Steps on one state run one after another (on one stream, or ordered by events). */

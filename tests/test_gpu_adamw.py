@@ -553,6 +553,57 @@ def test_captured_steps_count_on(eight):
     assert torch.equal(norm.out, out)
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_a_captured_step_with_copies_and_a_fork(eight):
+    """One graph: the gradients copied in, the norm, then the step on a second stream that joins before the conversion,
+    copies on either side of each. Replayed with new gradients it equals the eager calls; parameters may require gradients."""
+    rng = np.random.default_rng(11)
+    shapes = [(3000,), (40, 64), (7,)] + [(65,)] * 20
+    w0 = [dev((0.02 * rng.standard_normal(s)).astype(np.float32)) for s in shapes]
+    src = [torch.zeros(s, device="cuda") for s in shapes]
+
+    def build():
+        W = [torch.nn.Parameter(w.clone()) for w in w0]
+        G = [torch.zeros_like(w) for w in w0]
+        opt = S.AdamW(W, bits=8 if eight else 32, weight_decay=WD, seed=3, device_step=True)
+        other = S.AdamW(W, bits=32 if eight else 8, device_step=True)
+        norm = S.GradNorm(G, 0.5)
+        plan = S.AdamWPlan(opt, G, B1, B2, EPS, grad_scale=norm.coef, skip_if=norm.skip)
+        return W, G, opt, other, norm, plan, torch.zeros(shapes[0], device="cuda")
+
+    def body(W, G, opt, other, norm, plan, out, side):
+        for g, s in zip(G, src):
+            g.copy_(s)
+        norm.run()
+        norm.skip.add_(0)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            plan.run(LR)
+        torch.cuda.current_stream().wait_stream(side)
+        S.adamw_convert(opt, other)
+        out.copy_(W[0].detach())
+
+    a, b = build(), build()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body(*a, side)
+    for step in range(3):
+        for s in src:
+            s.normal_(std=0.1)
+        if step == 1:
+            src[1][3, 3] = math.inf
+        graph.replay()
+        body(*b, side)
+        torch.cuda.synchronize()
+        assert a[2].t == b[2].t == a[3].t == b[3].t == (1, 1, 2)[step]
+        assert torch.equal(a[6], b[6]) and torch.equal(a[4].out[1:], b[4].out[1:])
+        for x, y in zip(a[2:4], b[2:4]):
+            for k in ("W", "m", "v", "scales"):
+                for p, q in zip(getattr(x, k) or [], getattr(y, k) or []):
+                    assert torch.equal(p.detach().view(torch.uint8), q.detach().view(torch.uint8))
+
+
 def test_steps_on_another_stream():
     opt, G, refs, gs = make([(70000,), (33, 40)], True, F32, F32, False)
     side = torch.cuda.Stream()
