@@ -648,7 +648,7 @@ __device__ __forceinline__ uint32_t fetch_tile8(const AdTensor& T, int tile, int
 }
 
 // A tile with vector moments, 8-bit, a block to each half of the warp (sixteen entries a lane: what a block
-// costs beside its entries is then paid once for two): the same values as step_block8 with fewer instructions (370 a warp
+// costs beside its entries is then paid once for two): the same values as step_block8 with fewer instructions (395 a warp
 // for 256 entries, the first form took 770), which are what bounds it.
 //  - b1 m = (b1 2^k) code and b2 v = (b2 2^2k) code^2: a power of two commutes with the rounding, so the factor is
 //    formed once a block (while it is a normal number).
@@ -866,9 +866,10 @@ __global__ void __launch_bounds__(32 * kAd32Warps, 8) k_adamw32(const __grid_con
 // Each warp has two stages of its own: the next tile's operands are on their way into one (cp.async) while the other is
 // stepped. A CTA walks over a stretch of its own: tiles dealt out in turn over the grid took 2.35 ms instead of 2.20 on
 // the 774M-entry case with master (all CTAs load and store in step). Deeper rings (up to four stages: 2.35, 2.47 and 2.51
-// ms with two, three and four) and more warps with fewer registers measured slower. bf16 weights without a
-// master are bound by issue slots and HBM together: 65.6M entries take 134 to 141 us (4.7 to 4.9 TB/s), data that stays
-// in L2 would take 114 with the issue slots 78% busy.
+// ms with two, three and four) and more warps with fewer registers measured slower. bf16 weights without a master: 65.6M
+// entries take 137 to 141 us (4.7 to 4.8 TB/s), and no unit is full (issue slots 65%, FMA pipe 56%, ALU 49%, DRAM 51%). With
+// 16 warps an SM a third of the cycles has none to issue: of the 5.2 cycles between two instructions of a warp 1.3 are
+// the first one's latency, 0.7 a busy pipe, 1.0 other warps' turns. Data that stays in L2 would take 114 us.
 constexpr int kAd8Warps = 2, kAd8Ctas = 8;
 constexpr int kAd8Run = 24;  // tiles of a warp in a long run of CTAs
 template <int kKind, class Table>
